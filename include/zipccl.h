@@ -392,6 +392,107 @@ zipccl_status zipccl_profile_codec(const void* sample, uint64_t n, zipccl_plan_t
 zipccl_status zipccl_rs_choose(const zipccl_codec_profile_t* prof, const zipccl_link_t* link, int ranks,
                                uint64_t bytes, int* use_codec, double* native_us, double* zipped_us);
 
+/* ---- Mixture-of-experts rows (the MoE all-to-all of S2.D: what comes before and after the
+ * payload) ----
+ * A router gives each of `tokens` tokens `top_k` experts.  The choices are sorted by expert
+ * (zipccl_moe_sort: the row lists zipccl_compress_gather takes), the tokens' rows copied to
+ * their experts (zipccl_moe_dispatch; zipccl_quantize_rows in 8 bits), multiplied there
+ * (zipccl_experts_product) and summed back with weights (zipccl_moe_combine), with the
+ * gradients of dispatch and combine.
+ *   - Matrices are row-major with a row stride in values (>= row_len); pointers and strides
+ *     need the alignment of one value only, unless stated.  Outputs must not overlap inputs.
+ *   - dtype is ZIPCCL_BF16 or ZIPCCL_FP32.  Sums are fp32 in a fixed order, rounded once to
+ *     nearest even (a NaN result in BF16 is 0x7FC0); every result is the same on every run.
+ *   - slots[t * top_k + k] is the row of token t's k-th choice, or negative: the choice is
+ *     dropped and contributes nothing, whatever its weight.  A slot at or past the number
+ *     of rows sets ZIPCCL_STATUS_BAD_INDEX and counts as dropped.  Where rows are written by
+ *     slot (dispatch, combine_backward, quantize_rows) no two choices may share a slot, and
+ *     rows no slot names stay as they were.
+ *   - tokens == 0 or no rows is valid.  tokens * top_k and the number of rows are below 2^31,
+ *     row_len at most 2^28. */
+#define ZIPCCL_MAX_EXPERTS 1024
+#define ZIPCCL_MAX_TOP_K 64
+#define ZIPCCL_ROW_PAD 128
+#define ZIPCCL_MOE_SORT_WORKSPACE_BYTES (1u << 20)
+
+typedef enum zipccl_dtype { ZIPCCL_BF16 = 0, ZIPCCL_FP32 = 1 } zipccl_dtype;
+
+/* Sorts the choices by expert, stable: slots as above count the kept choices of smaller
+ * experts and the earlier kept choices (token-major) of the same one.
+ *   experts     device, tokens x top_k expert numbers, int32 or int64 (id_bytes 4 or 8), row
+ *               stride `stride`; negative numbers are dropped, numbers >= num_experts dropped
+ *               with ZIPCCL_STATUS_BAD_INDEX
+ *   offsets     device int32[num_experts + 1]: first row of each expert, then the kept total
+ *   rows        device int32[tokens * top_k]: token of each row; -1 from the kept total on
+ *   slots       device int32[tokens * top_k]
+ *   workspace   device scratch, 256-byte aligned, ZIPCCL_MOE_SORT_WORKSPACE_BYTES; carries
+ *               nothing between calls; concurrent calls need separate ones
+ * One launch up to 16384 choices, two above.
+ * Errors: INVALID (NULL pointers, top_k outside 1..ZIPCCL_MAX_TOP_K, num_experts outside
+ * 1..ZIPCCL_MAX_EXPERTS, id_bytes, stride < top_k), ALIGN, SIZE, HIP. */
+zipccl_status zipccl_moe_sort(const void* experts, int id_bytes, uint64_t stride, uint64_t tokens, int top_k,
+                              int num_experts, int32_t* offsets, int32_t* rows, int32_t* slots, void* workspace,
+                              uint64_t workspace_bytes, uint32_t* status, void* stream);
+
+/* y[slots[t][k]] = x[t], bits copied.  x: tokens rows; y: y_rows rows.
+ * Errors (this and the next three): INVALID (NULL pointers, top_k or row_len out of range,
+ * stride < row_len, dtype), ALIGN, SIZE, HIP. */
+zipccl_status zipccl_moe_dispatch(const void* x, uint64_t x_stride, const int32_t* slots, uint64_t tokens, int top_k,
+                                  uint64_t row_len, int dtype, void* y, uint64_t y_rows, uint64_t y_stride,
+                                  uint32_t* status, void* stream);
+
+/* Gradient of zipccl_moe_dispatch: dx[t] = sum over k, in order, of dy[slots[t][k]] (0 for a
+ * token without rows). */
+zipccl_status zipccl_moe_dispatch_backward(const void* dy, uint64_t dy_rows, uint64_t dy_stride, const int32_t* slots,
+                                           uint64_t tokens, int top_k, uint64_t row_len, int dtype, void* dx,
+                                           uint64_t dx_stride, uint32_t* status, void* stream);
+
+/* out[t] = sum over k, in order, of weights[t][k] * y[slots[t][k]] (0 for a token without
+ * rows).  weights: device fp32[tokens * top_k], or NULL for 1.  A dropped choice's weight is
+ * not read into the sum; a weight of 0 on a kept one multiplies as any other. */
+zipccl_status zipccl_moe_combine(const void* y, uint64_t y_rows, uint64_t y_stride, const int32_t* slots,
+                                 const float* weights, uint64_t tokens, int top_k, uint64_t row_len, int dtype,
+                                 void* out, uint64_t out_stride, uint32_t* status, void* stream);
+
+/* Gradient of zipccl_moe_combine for a gradient dout of its output:
+ *   dy[slots[t][k]] = weights[t][k] * dout[t]
+ *   dweights[t][k]  = sum over the row of dout[t] * y[slots[t][k]]   (0 for a dropped choice)
+ * y and dy: y_rows rows each; dweights: device fp32[tokens * top_k]. */
+zipccl_status zipccl_moe_combine_backward(const void* dout, uint64_t dout_stride, const void* y, uint64_t y_rows,
+                                          uint64_t y_stride, const int32_t* slots, const float* weights,
+                                          uint64_t tokens, int top_k, uint64_t row_len, int dtype, void* dy,
+                                          uint64_t dy_stride, float* dweights, uint32_t* status, void* stream);
+
+/* BF16 rows in 8 bits with a scale each, written to every slot of their token (slots NULL:
+ * row t of q is token t, and q_rows >= tokens; weights are laid out this way once).  With
+ * a = max |x[t][h]|:
+ *   q = rint(127 * x / a), half to even, exact;  scale = a / 127 in fp32
+ * (a = 0: q = 0 and scale 0; a row with a NaN or an infinity: q = 0 and scale NaN).
+ * q rows have q_stride bytes, a multiple of ZIPCCL_ROW_PAD, and are padded with zeros from
+ * row_len up to the next multiple of it.  q is 16-byte aligned; scales: device fp32[q_rows].
+ * Errors: as zipccl_moe_dispatch; ALIGN also for q_stride. */
+zipccl_status zipccl_quantize_rows(const void* x, uint64_t x_stride, uint64_t tokens, uint64_t row_len,
+                                   const int32_t* slots, int top_k, void* q, uint64_t q_rows, uint64_t q_stride,
+                                   float* scales, uint32_t* status, void* stream);
+
+/* The experts' product in 8-bit integers: for the rows s of expert e (offsets[e] <= s <
+ * offsets[e + 1]) and n < outputs
+ *   out[s][n] = float(sum over h of q[s][h] * w[e][n][h]) * scales[s] * w_scales[e][n]
+ * with exact 32-bit sums, rounded once to out_dtype.
+ *   q, scales     rows as zipccl_quantize_rows writes them (q_stride bytes, zero-padded)
+ *   w             device, num_experts * outputs rows of w_stride bytes in the same layout
+ *   w_scales      device fp32[num_experts * outputs]
+ *   offsets       device int32[num_experts + 1], ascending, as zipccl_moe_sort writes them;
+ *                 values outside 0..rows are clamped; NULL with num_experts == 1: all rows.
+ *                 Rows outside every expert's range are left as they were.
+ * Strides are multiples of ZIPCCL_ROW_PAD, q and w 16-byte aligned.
+ * Errors: INVALID, ALIGN, SIZE (row_len > 131071: sums could pass 32 bits; rows * outputs
+ * beyond one launch, about 2^36), HIP. */
+zipccl_status zipccl_experts_product(const void* q, uint64_t q_stride, const float* scales, uint64_t rows,
+                                     const void* w, uint64_t w_stride, const float* w_scales, int num_experts,
+                                     uint64_t outputs, uint64_t row_len, const int32_t* offsets, void* out,
+                                     uint64_t out_stride, int out_dtype, uint32_t* status, void* stream);
+
 /* Static text for a status code. */
 const char* zipccl_strerror(zipccl_status s);
 

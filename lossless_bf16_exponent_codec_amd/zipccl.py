@@ -19,6 +19,8 @@ OK, ERR_INVALID, ERR_ALIGN, ERR_SIZE, ERR_HIP, ERR_CORRUPT = range(6)
 STATUS_ESC_OVERFLOW, STATUS_CORRUPT, STATUS_BAD_INDEX, STATUS_WAIT_LIMIT = 1, 2, 4, 8
 MAX_SEGMENTS, MAX_PEERS = 64, 16
 FORMAT_VERSION, MAGIC = 1, 0x3143435A
+MAX_EXPERTS, MAX_TOP_K, ROW_PAD, MOE_SORT_WORKSPACE_BYTES = 1024, 64, 128, 1 << 20
+BF16, FP32 = 0, 1
 
 
 class PlanT(ctypes.Structure):
@@ -115,6 +117,21 @@ def _load() -> ctypes.CDLL:
     lib.zipccl_rs_choose.argtypes = [ctypes.POINTER(CodecProfileT), ctypes.POINTER(LinkT), i32, u64,
                                      ctypes.POINTER(i32), ctypes.POINTER(ctypes.c_double),
                                      ctypes.POINTER(ctypes.c_double)]
+    lib.zipccl_moe_sort.restype = i32
+    lib.zipccl_moe_sort.argtypes = [vp, i32, u64, u64, i32, i32, vp, vp, vp, vp, u64, vp, vp]
+    lib.zipccl_moe_dispatch.restype = i32
+    lib.zipccl_moe_dispatch.argtypes = [vp, u64, vp, u64, i32, u64, i32, vp, u64, u64, vp, vp]
+    lib.zipccl_moe_dispatch_backward.restype = i32
+    lib.zipccl_moe_dispatch_backward.argtypes = [vp, u64, u64, vp, u64, i32, u64, i32, vp, u64, vp, vp]
+    lib.zipccl_moe_combine.restype = i32
+    lib.zipccl_moe_combine.argtypes = [vp, u64, u64, vp, vp, u64, i32, u64, i32, vp, u64, vp, vp]
+    lib.zipccl_moe_combine_backward.restype = i32
+    lib.zipccl_moe_combine_backward.argtypes = [vp, u64, vp, u64, u64, vp, vp, u64, i32, u64, i32, vp, u64, vp, vp,
+                                                vp]
+    lib.zipccl_quantize_rows.restype = i32
+    lib.zipccl_quantize_rows.argtypes = [vp, u64, u64, u64, vp, i32, vp, u64, u64, vp, vp, vp]
+    lib.zipccl_experts_product.restype = i32
+    lib.zipccl_experts_product.argtypes = [vp, u64, vp, u64, vp, u64, vp, i32, u64, u64, vp, vp, u64, i32, vp, vp]
     lib.zipccl_pipeline_scratch_size.restype = u64
     lib.zipccl_pipeline_scratch_size.argtypes = [i32, u64]
     lib.zipccl_pipeline_create.restype = i32
@@ -519,6 +536,142 @@ class Pipeline:
 
     def __del__(self):
         self.close()
+
+
+# ------------------------------------------------------------------------------------
+# mixture-of-experts rows
+# ------------------------------------------------------------------------------------
+_DTYPES = {torch.bfloat16: BF16, torch.float32: FP32}
+
+
+def _matrix(t, what, dtype=None):
+    """(address, row stride) of a 2-D row-major tensor."""
+    if t.dim() != 2 or (t.numel() > 0 and t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} is a 2-D tensor with contiguous rows")
+    if t.dtype not in _DTYPES if dtype is None else t.dtype != dtype:
+        raise ValueError(f"{what} is {t.dtype}")
+    return t.data_ptr(), max(t.stride(0), t.shape[1])
+
+
+def _vector(t, n, dtype, what):
+    """Address of a contiguous tensor of at least n values."""
+    if t.dtype != dtype or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{what} is a contiguous {dtype} tensor of at least {n} values")
+    return t.data_ptr()
+
+
+def _slots(slots, tokens, what="slots"):
+    if slots.dim() != 2 or slots.shape[0] != tokens:
+        raise ValueError(f"{what} is tokens x top_k, {tokens} tokens")
+    return _vector(slots, 0, torch.int32, what), slots.shape[1]
+
+
+def _same_rows(a, b, what):
+    if a.shape[1] != b.shape[1] or a.dtype != b.dtype:
+        raise ValueError(f"{what} have the same row length and dtype")
+
+
+def moe_sort(experts, num_experts: int, offsets, rows, slots, workspace, status=None, stream=None):
+    """zipccl_moe_sort.  experts: int32 or int64 device tensor, tokens x top_k (a router's
+    top-k indices; negative: dropped).  Writes offsets (int32, num_experts + 1), rows
+    (int32, tokens * top_k) and slots (int32, tokens x top_k).  workspace:
+    MOE_SORT_WORKSPACE_BYTES device bytes."""
+    if experts.dim() != 2 or experts.dtype not in (torch.int32, torch.int64) or \
+            (experts.numel() > 0 and experts.shape[1] > 1 and experts.stride(1) != 1):
+        raise ValueError("experts is a 2-D int32 or int64 tensor with contiguous rows")
+    T, K = experts.shape
+    _check(_lib.zipccl_moe_sort(experts.data_ptr(), experts.element_size(), max(experts.stride(0), K), T, K,
+                                num_experts, _vector(offsets, num_experts + 1, torch.int32, "offsets"),
+                                _vector(rows, T * K, torch.int32, "rows"),
+                                _vector(slots, T * K, torch.int32, "slots"), workspace.data_ptr(),
+                                _nbytes(workspace), _ptr(status), _stream(stream)), "zipccl_moe_sort")
+
+
+def moe_dispatch(x, slots, y, status=None, stream=None):
+    """zipccl_moe_dispatch: y[slots[t, k]] = x[t]."""
+    xp, xs = _matrix(x, "x")
+    yp, ys = _matrix(y, "y")
+    _same_rows(x, y, "x and y")
+    sp, K = _slots(slots, x.shape[0])
+    _check(_lib.zipccl_moe_dispatch(xp, xs, sp, x.shape[0], K, x.shape[1], _DTYPES[x.dtype], yp, y.shape[0], ys,
+                                    _ptr(status), _stream(stream)), "zipccl_moe_dispatch")
+
+
+def moe_dispatch_backward(dy, slots, dx, status=None, stream=None):
+    """zipccl_moe_dispatch_backward: dx[t] = sum over k of dy[slots[t, k]]."""
+    yp, ys = _matrix(dy, "dy")
+    xp, xs = _matrix(dx, "dx")
+    _same_rows(dy, dx, "dy and dx")
+    sp, K = _slots(slots, dx.shape[0])
+    _check(_lib.zipccl_moe_dispatch_backward(yp, dy.shape[0], ys, sp, dx.shape[0], K, dx.shape[1],
+                                             _DTYPES[dy.dtype], xp, xs, _ptr(status), _stream(stream)),
+           "zipccl_moe_dispatch_backward")
+
+
+def moe_combine(y, slots, weights, out, status=None, stream=None):
+    """zipccl_moe_combine: out[t] = sum over k of weights[t, k] * y[slots[t, k]] (weights
+    float32, or None for 1)."""
+    yp, ys = _matrix(y, "y")
+    op, os_ = _matrix(out, "out")
+    _same_rows(y, out, "y and out")
+    sp, K = _slots(slots, out.shape[0])
+    wp = None if weights is None else _vector(weights, out.shape[0] * K, torch.float32, "weights")
+    _check(_lib.zipccl_moe_combine(yp, y.shape[0], ys, sp, wp, out.shape[0], K, out.shape[1], _DTYPES[y.dtype], op,
+                                   os_, _ptr(status), _stream(stream)), "zipccl_moe_combine")
+
+
+def moe_combine_backward(dout, y, slots, weights, dy, dweights, status=None, stream=None):
+    """zipccl_moe_combine_backward: dy[slots[t, k]] = weights[t, k] * dout[t] and
+    dweights[t, k] = <dout[t], y[slots[t, k]]>."""
+    gp, gs = _matrix(dout, "dout")
+    yp, ys = _matrix(y, "y")
+    dp, ds = _matrix(dy, "dy")
+    _same_rows(dout, y, "dout and y")
+    _same_rows(y, dy, "y and dy")
+    if y.shape[0] != dy.shape[0]:
+        raise ValueError("y and dy have the same rows")
+    T = dout.shape[0]
+    sp, K = _slots(slots, T)
+    _check(_lib.zipccl_moe_combine_backward(gp, gs, yp, y.shape[0], ys, sp,
+                                            _vector(weights, T * K, torch.float32, "weights"), T, K, y.shape[1],
+                                            _DTYPES[y.dtype], dp, ds,
+                                            _vector(dweights, T * K, torch.float32, "dweights"), _ptr(status),
+                                            _stream(stream)), "zipccl_moe_combine_backward")
+
+
+def quantize_rows(x, q, scales, slots=None, status=None, stream=None):
+    """zipccl_quantize_rows: BF16 rows x to int8 rows q (row stride a multiple of ROW_PAD,
+    at least as long as x's rows) with float32 scales, to every slot of a token or, without
+    slots, row by row."""
+    xp, xs = _matrix(x, "x", torch.bfloat16)
+    qp, qs = _matrix(q, "q", torch.int8)
+    if q.shape[1] < x.shape[1]:
+        raise ValueError("q's rows hold x's rows")
+    sp, K = (None, 1) if slots is None else _slots(slots, x.shape[0])
+    _check(_lib.zipccl_quantize_rows(xp, xs, x.shape[0], x.shape[1], sp, K, qp, q.shape[0], qs,
+                                     _vector(scales, q.shape[0], torch.float32, "scales"), _ptr(status),
+                                     _stream(stream)), "zipccl_quantize_rows")
+
+
+def experts_product(q, scales, w, w_scales, row_len: int, out, offsets=None, status=None, stream=None):
+    """zipccl_experts_product.  q: int8 rows with scales, sorted by expert; w: int8,
+    experts x outputs x stride (or outputs x stride for one), w_scales float32, experts x
+    outputs; row_len: values of a row without its padding; out: rows x outputs, bfloat16
+    or float32; offsets: int32, experts + 1 (None: one expert)."""
+    qp, qs = _matrix(q, "q", torch.int8)
+    op, os_ = _matrix(out, "out")
+    if w.dim() not in (2, 3) or w.dtype != torch.int8 or not w.is_contiguous():
+        raise ValueError("w is a contiguous int8 tensor, experts x outputs x row stride")
+    E, N = (1 if w.dim() == 2 else w.shape[0]), w.shape[-2]
+    if out.shape[0] != q.shape[0] or out.shape[1] != N:
+        raise ValueError("out is q's rows x w's outputs")
+    if row_len > q.shape[1] or row_len > w.shape[-1]:
+        raise ValueError("row_len is at most the row length of q and w")
+    _check(_lib.zipccl_experts_product(qp, qs, _vector(scales, q.shape[0], torch.float32, "scales"), q.shape[0],
+                                       w.data_ptr(), w.shape[-1], _vector(w_scales, E * N, torch.float32, "w_scales"),
+                                       E, N, row_len, None if offsets is None else
+                                       _vector(offsets, E + 1, torch.int32, "offsets"), op, os_, _DTYPES[out.dtype],
+                                       _ptr(status), _stream(stream)), "zipccl_experts_product")
 
 
 # ------------------------------------------------------------------------------------
