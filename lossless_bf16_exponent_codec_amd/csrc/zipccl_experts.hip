@@ -18,6 +18,7 @@ namespace zc {
 namespace {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v16i __attribute__((ext_vector_type(16)));
 
 __device__ inline uint32_t lane_id() { return __lane_id(); }
 
@@ -139,6 +140,20 @@ __device__ inline void expert_rows(const ProductArgs& a, uint32_t e, uint32_t& b
     end = uint32_t(min(max(hi, int64_t(begin)), int64_t(a.rows)));
 }
 
+// Row tiles of kRows rows of all experts.
+template <uint32_t kRows>
+__device__ inline uint32_t count_tiles(const ProductArgs& a)
+{
+    uint32_t sum = 0;
+    for (uint32_t e = lane_id(); e < a.experts; e += 64) {
+        uint32_t begin, end;
+        expert_rows(a, e, begin, end);
+        sum += (end - begin + kRows - 1) / kRows;
+    }
+    for (uint32_t d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+    return __builtin_amdgcn_readfirstlane(sum);
+}
+
 // The expert and the rows of row tile `tile`, tiles of kRows rows counted expert after
 // expert.  Every wave looks for itself: 64 experts at a time, a running sum over lanes.
 // False past the last tile.
@@ -203,75 +218,152 @@ __device__ inline void store4(const ProductArgs& a, uint32_t row, uint32_t n, v4
     }
 }
 
-constexpr uint32_t kTileRows = 128, kTileOuts = 128, kTileThreads = 256;
-
-// 16-byte piece `piece` of row `row` in a slab of 128-byte rows, spread over the banks.
-__device__ inline uint32_t lds_at(uint32_t row, uint32_t piece) { return row * 128 + ((piece ^ (row >> 1)) & 7) * 16; }
-
-// A tile of 128 rows x 128 outputs per workgroup, 64 x 64 per wave.  Slabs of 128 values
-// along the rows go through registers into LDS.  Rows past the expert's end repeat its
-// last row and are not stored.
-__global__ __launch_bounds__(kTileThreads) void product_kernel(const ProductArgs a)
+// All waves: n loads may still be in flight (the oldest have landed), no LDS read is, and
+// nothing moves across.
+template <uint32_t N>
+__device__ inline void wait_loads_and_meet()
 {
-    __shared__ __attribute__((aligned(16))) uint8_t s_q[kTileRows * 128];
-    __shared__ __attribute__((aligned(16))) uint8_t s_w[kTileOuts * 128];
-    uint32_t expert, row0, rows;
-    const uint32_t across = (a.outputs + kTileOuts - 1) / kTileOuts;
-    if (!find_tile<kTileRows>(a, blockIdx.x / across, expert, row0, rows)) return;
-    const uint32_t n0 = blockIdx.x % across * kTileOuts;
-    const uint32_t tid = threadIdx.x, lane = lane_id();
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const uint32_t wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
-    const int8_t* w = a.w + uint64_t(expert) * a.outputs * a.w_stride;
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
 
-    const uint32_t piece = tid & 7, r0 = tid >> 3;   // this thread's 16 bytes in rows r0, r0 + 32, ...
-    v4i acc[4][4] = {};
-    uint4 vq[4], vw[4];
-    const auto load = [&](uint32_t slab) {
+template <uint32_t N>
+__device__ inline void wait_loads()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
+typedef __attribute__((address_space(1))) const void global_void;
+typedef __attribute__((address_space(3))) void lds_void;
+
+// 16 bytes per lane from global memory to LDS: lane l's land at `to` + 16 l.
+__device__ inline void load_lds(const int8_t* from, uint8_t* to)
+{
+    __builtin_amdgcn_global_load_lds((global_void*)from, (lds_void*)to, 16, 0, 0);
+}
+
+// The share of the tiles this workgroup takes.  Workgroups go to the 8 XCDs in turn; each
+// XCD takes a run of consecutive tiles, and tiles run over kBand row tiles, then over the
+// outputs, so that those an XCD works on at one time share rows and weights in its L2.
+constexpr uint32_t kXcds = 8, kBand = 4;
+
+template <uint32_t kRows>
+__device__ inline bool take_tile(const ProductArgs& a, uint32_t across, uint32_t& expert, uint32_t& row0,
+                                 uint32_t& rows, uint32_t& column)
+{
+    const uint32_t down = count_tiles<kRows>(a), total = down * across;
+    const uint32_t per = (total + kXcds - 1) / kXcds;
+    const uint32_t at = blockIdx.x / kXcds, t = blockIdx.x % kXcds * per + at;
+    if (at >= per || t >= total) return false;
+    const uint32_t band = t / (kBand * across), in = t % (kBand * across);
+    const uint32_t high = min(kBand, down - band * kBand);
+    column = in / high;
+    return find_tile<kRows>(a, band * kBand + in % high, expert, row0, rows);
+}
+
+// A tile of 64 kM rows x 64 kN outputs per workgroup of 4 waves, each 32 kM x 32 kN.  The
+// rows go through LDS in steps of 64 values, four steps deep: step h + 4 is requested
+// into the place of step h once every wave holds step h in registers, and while a wave
+// multiplies step h it reads step h + 1 from LDS.  One barrier per step.
+constexpr uint32_t kTileThreads = 256;
+constexpr uint32_t kStep = 64, kStages = 4;
+
+template <uint32_t kM, uint32_t kN>
+__global__ __launch_bounds__(kTileThreads, kM * kN > 8 ? 1 : 2) void product_tile_kernel(const ProductArgs a)
+{
+    constexpr uint32_t kRows = 64 * kM, kOuts = 64 * kN;
+    constexpr uint32_t kStage = (kRows + kOuts) * kStep, kLoads = kM + kN;   // bytes, loads per thread of a step
+    extern __shared__ __attribute__((aligned(1024))) uint8_t s_stage[];
+    const uint32_t across = (a.outputs + kOuts - 1) / kOuts;
+    uint32_t expert, row0, rows, column;
+    if (!take_tile<kRows>(a, across, expert, row0, rows, column)) return;
+    const uint32_t n0 = column * kOuts;
+    const uint32_t lane = lane_id();
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int8_t* w = a.w + (uint64_t(expert) * a.outputs + n0) * a.w_stride;
+
+    // A load of a wave fills 16 rows of 64 bytes.  The 16-byte pieces of a row are
+    // swapped by bits 2-3 of the row so that 16 lanes reading one piece of 16 rows use
+    // every bank.  Rows past the tile's end repeat its last one and are not stored.
+    const int8_t* from[kLoads];
+    const uint32_t r = 16 * wave + lane / 4, piece = (lane & 3) ^ ((lane >> 4) & 3);
 #pragma unroll
-        for (uint32_t i = 0; i < 4; i++) {
-            const uint32_t r = min(r0 + 32 * i, rows - 1), n = min(n0 + r0 + 32 * i, a.outputs - 1);
-            vq[i] = *reinterpret_cast<const uint4*>(a.q + uint64_t(row0 + r) * a.q_stride + slab * 128 + piece * 16);
-            vw[i] = *reinterpret_cast<const uint4*>(w + uint64_t(n) * a.w_stride + slab * 128 + piece * 16);
+    for (uint32_t i = 0; i < kLoads; i++)
+        from[i] = (i < kM ? a.q + uint64_t(row0 + min(r + 64 * i, rows - 1)) * a.q_stride
+                          : w + uint64_t(min(r + 64 * (i - kM), a.outputs - 1 - n0)) * a.w_stride) + 16 * piece;
+    const uint32_t steps = 2 * a.slabs;
+    const auto load = [&](uint32_t step) {
+        const uint32_t at = min(step, steps - 1) * kStep;   // past the end: the last step again, never used
+        uint8_t* to = s_stage + (step % kStages) * kStage + 1024 * wave;
+#pragma unroll
+        for (uint32_t i = 0; i < kLoads; i++) load_lds(from[i] + at, to + 4096 * i);
+    };
+
+    const uint32_t wm = (wave >> 1) * 32 * kM, wn = (wave & 1) * 32 * kN;
+    const uint32_t half = lane >> 5, turn = (lane >> 2) & 3;
+    const uint8_t* read_q = s_stage + (wm + (lane & 31)) * kStep;
+    const uint8_t* read_w = s_stage + (kRows + wn + (lane & 31)) * kStep;
+    v16i acc[kM][kN] = {};
+    v4i fq[2][2][kM], fw[2][2][kN];
+    const auto read = [&](uint32_t to, uint32_t step) {
+        const uint32_t base = (step % kStages) * kStage;
+#pragma unroll
+        for (uint32_t k = 0; k < 2; k++) {
+            const uint32_t at = base + ((2 * k + half) ^ turn) * 16;
+#pragma unroll
+            for (uint32_t i = 0; i < kM; i++) fq[to][k][i] = *reinterpret_cast<const v4i*>(read_q + at + 32 * kStep * i);
+#pragma unroll
+            for (uint32_t j = 0; j < kN; j++) fw[to][k][j] = *reinterpret_cast<const v4i*>(read_w + at + 32 * kStep * j);
         }
     };
-    load(0);
-    for (uint32_t slab = 0; slab < a.slabs; slab++) {
-        __syncthreads();
+
+    for (uint32_t h = 0; h < kStages; h++) load(h);
+    wait_loads_and_meet<(kStages - 1) * kLoads>();
+    read(0, 0);
+    for (uint32_t h0 = 0; h0 < steps; h0 += 2) {
 #pragma unroll
-        for (uint32_t i = 0; i < 4; i++) {
-            *reinterpret_cast<uint4*>(s_q + lds_at(r0 + 32 * i, piece)) = vq[i];
-            *reinterpret_cast<uint4*>(s_w + lds_at(r0 + 32 * i, piece)) = vw[i];
-        }
-        __syncthreads();
-        if (slab + 1 < a.slabs) load(slab + 1);
+        for (uint32_t u = 0; u < 2; u++) {
+            wait_loads_and_meet<(kStages - 2) * kLoads>();
+            load(h0 + u + kStages);
+            read(u ^ 1, h0 + u + 1);
 #pragma unroll
-        for (uint32_t half = 0; half < 2; half++) {
-            v4i fq[4], fw[4];
+            for (uint32_t k = 0; k < 2; k++)
 #pragma unroll
-            for (uint32_t i = 0; i < 4; i++) {
-                fq[i] = *reinterpret_cast<const v4i*>(s_q + lds_at(wm + 16 * i + (lane & 15), 4 * half + (lane >> 4)));
-                fw[i] = *reinterpret_cast<const v4i*>(s_w + lds_at(wn + 16 * i + (lane & 15), 4 * half + (lane >> 4)));
+                for (uint32_t i = 0; i < kM; i++)
+#pragma unroll
+                    for (uint32_t j = 0; j < kN; j++)
+                        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[u][k][j], fq[u][k][i], acc[i][j], 0, 0, 0);
+            // the loads and LDS reads between the products, not before them
+            constexpr uint32_t kEach = kM * kN / kLoads > 0 ? kM * kN / kLoads : 1;
+#pragma unroll
+            for (uint32_t g = 0; g < kLoads; g++) {
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, kEach, 0);
             }
 #pragma unroll
-            for (uint32_t i = 0; i < 4; i++)
-#pragma unroll
-                for (uint32_t j = 0; j < 4; j++)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[j], fq[i], acc[i][j], 0, 0, 0);
+            for (uint32_t g = 0; g < kLoads; g++) {
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, kEach, 0);
+            }
         }
     }
-    // lane l holds outputs 4 (l / 16) .. + 3 of row l % 16 of each 16 x 16 piece
+    wait_loads<0>();   // the surplus loads land before the workgroup gives its LDS up
+
+    // lane l holds, of each 32 x 32 piece, row l % 32 and outputs 8 g + 4 (l / 32) .. + 3
     const float* ws = a.w_scales + uint64_t(expert) * a.outputs;
 #pragma unroll
-    for (uint32_t i = 0; i < 4; i++) {
-        const uint32_t r = wm + 16 * i + (lane & 15);
-        if (r >= rows) continue;
-        const float scale = a.scales[row0 + r];
+    for (uint32_t i = 0; i < kM; i++) {
+        const uint32_t row = wm + 32 * i + (lane & 31);
+        if (row >= rows) continue;
+        const float scale = a.scales[row0 + row];
 #pragma unroll
-        for (uint32_t j = 0; j < 4; j++) {
-            const uint32_t n = n0 + wn + 16 * j + 4 * (lane >> 4);
-            if (n < a.outputs) store4(a, row0 + r, n, acc[i][j], scale, ws);
-        }
+        for (uint32_t j = 0; j < kN; j++)
+#pragma unroll
+            for (uint32_t g = 0; g < 4; g++) {
+                const uint32_t n = n0 + wn + 32 * j + 8 * g + 4 * half;
+                const v4i v = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+                if (n < a.outputs) store4(a, row0 + row, n, v, scale, ws);
+            }
     }
 }
 
@@ -291,15 +383,43 @@ hipError_t launch_quantize_rows(const QuantArgs& a, hipStream_t s)
     return hipGetLastError();
 }
 
+namespace {
+
+// Tile shapes (in units of 64 x 64).
+constexpr uint32_t kLargeM = 4, kLargeN = 4;
+constexpr uint32_t kSmallM = 2, kSmallN = 2;
+
+uint64_t tile_workgroups(const ProductArgs& a, uint32_t m, uint32_t n)
+{
+    return (most_tiles(a, 64 * m) * ((a.outputs + 64 * n - 1) / (64 * n)) + kXcds - 1) / kXcds * kXcds;
+}
+
+template <uint32_t kM, uint32_t kN>
+hipError_t launch_tiles(const ProductArgs& a, hipStream_t s)
+{
+    constexpr uint32_t lds = kStages * 64 * (kM + kN) * kStep;
+    const auto kernel = product_tile_kernel<kM, kN>;
+    if (lds > 65536) {
+        if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, int(lds)))
+            return e;
+    }
+    hipLaunchKernelGGL(kernel, dim3(uint32_t(tile_workgroups(a, kM, kN))), dim3(kTileThreads), lds, s, a);
+    return hipGetLastError();
+}
+
+bool use_large(const ProductArgs& a) { return tile_workgroups(a, kLargeM, kLargeN) >= 256; }
+
+}  // namespace
+
 uint64_t product_workgroups(const ProductArgs& a)
 {
-    return most_tiles(a, kTileRows) * ((a.outputs + kTileOuts - 1) / kTileOuts);
+    return use_large(a) ? tile_workgroups(a, kLargeM, kLargeN) : tile_workgroups(a, kSmallM, kSmallN);
 }
 
 hipError_t launch_experts_product(const ProductArgs& a, hipStream_t s)
 {
-    hipLaunchKernelGGL(product_kernel, dim3(uint32_t(product_workgroups(a))), dim3(kTileThreads), 0, s, a);
-    return hipGetLastError();
+    return use_large(a) ? launch_tiles<kLargeM, kLargeN>(a, s) : launch_tiles<kSmallM, kSmallN>(a, s);
 }
 
 }  // namespace zc
