@@ -186,37 +186,50 @@ __device__ inline bool find_tile(const ProductArgs& a, uint32_t tile, uint32_t& 
     return false;
 }
 
-// One value's 4 neighbours along the outputs: scaled, rounded and stored.
-__device__ inline void store4(const ProductArgs& a, uint32_t row, uint32_t n, v4i acc, float scale, const float* ws)
-{
-    const uint64_t at = uint64_t(row) * a.out_stride + n;
-    float f[4];
+// 8 consecutive outputs from n on: sums of a row scaled, rounded and stored.
+struct Outputs {
+    float ws[8];
+    uint32_t n, count;
+
+    __device__ inline Outputs(const ProductArgs& a, uint32_t expert, uint32_t first)
+        : n(first), count(first < a.outputs ? min(8u, a.outputs - first) : 0u)
+    {
+        const float* from = a.w_scales + uint64_t(expert) * a.outputs + n;
 #pragma unroll
-    for (uint32_t r = 0; r < 4; r++) f[r] = n + r < a.outputs ? float(acc[r]) * scale * ws[n + r] : 0.0f;
-    if (a.fp32) {
-        float* o = reinterpret_cast<float*>(a.out) + at;
-        if (n + 4 <= a.outputs) {
-            __builtin_memcpy(o, f, 16);
+        for (uint32_t r = 0; r < 8; r++) ws[r] = r < count ? from[r] : 0.0f;
+    }
+
+    __device__ inline void store(const ProductArgs& a, uint32_t row, v4i lo, v4i hi) const
+    {
+        const float scale = a.scales[row];
+        const uint64_t at = uint64_t(row) * a.out_stride + n;
+        float f[8];
+#pragma unroll
+        for (uint32_t r = 0; r < 8; r++) f[r] = float(r < 4 ? lo[r & 3] : hi[r & 3]) * scale * ws[r];
+        if (a.fp32) {
+            float* o = reinterpret_cast<float*>(a.out) + at;
+            if (count == 8) {
+                __builtin_memcpy(o, f, 32);
+            } else {
+#pragma unroll
+                for (uint32_t r = 0; r < 7; r++)
+                    if (r < count) o[r] = f[r];
+            }
         } else {
+            uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + at;
+            uint32_t b[4];
 #pragma unroll
-            for (uint32_t r = 0; r < 4; r++)
-                if (n + r < a.outputs) o[r] = f[r];
-        }
-    } else {
-        uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + at;
-        uint32_t b[4];
+            for (uint32_t r = 0; r < 4; r++) b[r] = bf16_rne(f[2 * r]) | bf16_rne(f[2 * r + 1]) << 16;
+            if (count == 8) {
+                __builtin_memcpy(o, b, 16);
+            } else {
 #pragma unroll
-        for (uint32_t r = 0; r < 4; r++) b[r] = bf16_rne(f[r]);
-        if (n + 4 <= a.outputs) {
-            const uint2 v = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
-            __builtin_memcpy(o, &v, 8);
-        } else {
-#pragma unroll
-            for (uint32_t r = 0; r < 4; r++)
-                if (n + r < a.outputs) o[r] = uint16_t(b[r]);
+                for (uint32_t r = 0; r < 7; r++)
+                    if (r < count) o[r] = uint16_t(b[r >> 1] >> (16 * (r & 1)));
+            }
         }
     }
-}
+};
 
 // All waves: n loads may still be in flight (the oldest have landed), no LDS read is, and
 // nothing moves across.
@@ -224,12 +237,6 @@ template <uint32_t N>
 __device__ inline void wait_loads_and_meet()
 {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
-
-template <uint32_t N>
-__device__ inline void wait_loads()
-{
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
 }
 
 typedef __attribute__((address_space(1))) const void global_void;
@@ -272,6 +279,9 @@ __global__ __launch_bounds__(kTileThreads, kM * kN > 8 ? 1 : 2) void product_til
 {
     constexpr uint32_t kRows = 64 * kM, kOuts = 64 * kN;
     constexpr uint32_t kStage = (kRows + kOuts) * kStep, kLoads = kM + kN;   // bytes, loads per thread of a step
+    // LDS reads go between the first half of a step's products, loads between the second
+    constexpr uint32_t kHalf = kM * kN;
+    constexpr uint32_t kReadEach = (2 * kLoads + kHalf - 1) / kHalf, kLoadEach = kHalf > kLoads ? kHalf / kLoads : 1;
     extern __shared__ __attribute__((aligned(1024))) uint8_t s_stage[];
     const uint32_t across = (a.outputs + kOuts - 1) / kOuts;
     uint32_t expert, row0, rows, column;
@@ -323,8 +333,8 @@ __global__ __launch_bounds__(kTileThreads, kM * kN > 8 ? 1 : 2) void product_til
 #pragma unroll
         for (uint32_t u = 0; u < 2; u++) {
             wait_loads_and_meet<(kStages - 2) * kLoads>();
-            load(h0 + u + kStages);
             read(u ^ 1, h0 + u + 1);
+            load(h0 + u + kStages);
 #pragma unroll
             for (uint32_t k = 0; k < 2; k++)
 #pragma unroll
@@ -332,38 +342,48 @@ __global__ __launch_bounds__(kTileThreads, kM * kN > 8 ? 1 : 2) void product_til
 #pragma unroll
                     for (uint32_t j = 0; j < kN; j++)
                         acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[u][k][j], fq[u][k][i], acc[i][j], 0, 0, 0);
-            // the loads and LDS reads between the products, not before them
-            constexpr uint32_t kEach = kM * kN / kLoads > 0 ? kM * kN / kLoads : 1;
+#pragma unroll
+            for (uint32_t g = 0; g < kHalf; g++) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, kReadEach, 0);
+            }
 #pragma unroll
             for (uint32_t g = 0; g < kLoads; g++) {
+                __builtin_amdgcn_sched_group_barrier(0x008, kLoadEach, 0);
                 __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x008, kEach, 0);
             }
-#pragma unroll
-            for (uint32_t g = 0; g < kLoads; g++) {
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x008, kEach, 0);
-            }
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
-    wait_loads<0>();   // the surplus loads land before the workgroup gives its LDS up
+    wait_loads_and_meet<0>();   // the surplus loads have landed: LDS is free
 
-    // lane l holds, of each 32 x 32 piece, row l % 32 and outputs 8 g + 4 (l / 32) .. + 3
-    const float* ws = a.w_scales + uint64_t(expert) * a.outputs;
+    // Lane l holds, of each 32 x 32 piece, row l % 32 and outputs 8 g + 4 (l / 32) .. + 3.
+    // Strips of 32 rows change hands in the wave's own part of LDS so that a lane gets 8
+    // outputs in a row and a store covers whole rows of the wave's outputs.
+    constexpr uint32_t kPitch = 32 * kN * 4 + 16;       // bytes; the 16 spread rows over the banks
+    constexpr uint32_t kPerRow = 4 * kN;                // lanes of a row
+    uint8_t* strip = s_stage + wave * (32 * kPitch);
+    const uint32_t n = n0 + wn + 8 * (lane % kPerRow);
+    const Outputs to(a, expert, n);
 #pragma unroll
     for (uint32_t i = 0; i < kM; i++) {
-        const uint32_t row = wm + 32 * i + (lane & 31);
-        if (row >= rows) continue;
-        const float scale = a.scales[row0 + row];
+        if (wm + 32 * i >= rows) break;
 #pragma unroll
         for (uint32_t j = 0; j < kN; j++)
 #pragma unroll
             for (uint32_t g = 0; g < 4; g++) {
-                const uint32_t n = n0 + wn + 32 * j + 8 * g + 4 * half;
                 const v4i v = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
-                if (n < a.outputs) store4(a, row0 + row, n, v, scale, ws);
+                *reinterpret_cast<v4i*>(strip + (lane & 31) * kPitch + (32 * j + 8 * g + 4 * half) * 4) = v;
             }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+        for (uint32_t at = lane / kPerRow; at < 32; at += 64 / kPerRow) {
+            const uint32_t row = wm + 32 * i + at;
+            if (row >= rows) break;
+            const v4i* v = reinterpret_cast<const v4i*>(strip + at * kPitch + 32 * (lane % kPerRow));
+            to.store(a, row0 + row, v[0], v[1]);
+        }
+        __builtin_amdgcn_wave_barrier();
     }
 }
 
