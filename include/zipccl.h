@@ -485,7 +485,8 @@ zipccl_status zipccl_quantize_rows(const void* x, uint64_t x_stride, uint64_t to
  *   offsets       device int32[num_experts + 1], ascending, as zipccl_moe_sort writes them;
  *                 values outside 0..rows are clamped; NULL with num_experts == 1: all rows.
  *                 Rows outside every expert's range are left as they were.
- * Strides are multiples of ZIPCCL_ROW_PAD, q and w 16-byte aligned.
+ * Strides of q and w are multiples of ZIPCCL_ROW_PAD, at most 2^24; q and w are 16-byte
+ * aligned.
  * Errors: INVALID, ALIGN, SIZE (row_len > 131071: sums could pass 32 bits; rows * outputs
  * beyond one launch, about 2^36), HIP. */
 zipccl_status zipccl_experts_product(const void* q, uint64_t q_stride, const float* scales, uint64_t rows,

@@ -10,6 +10,7 @@
 // which tiles and waves add them does not show.
 #include <hip/hip_runtime.h>
 
+#include <cstdlib>
 #include "zipccl.h"
 #include "zipccl_moe_internal.h"
 
@@ -19,6 +20,7 @@ namespace {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v16i __attribute__((ext_vector_type(16)));
+typedef float v4f __attribute__((ext_vector_type(4)));
 
 __device__ inline uint32_t lane_id() { return __lane_id(); }
 
@@ -140,53 +142,63 @@ __device__ inline void expert_rows(const ProductArgs& a, uint32_t e, uint32_t& b
     end = uint32_t(min(max(hi, int64_t(begin)), int64_t(a.rows)));
 }
 
-// Row tiles of kRows rows of all experts.
+// Row tiles of kRows rows, counted expert after expert.  Every wave works them out for
+// itself from the offsets: lane l looks at experts l, 64 + l, ...
 template <uint32_t kRows>
-__device__ inline uint32_t count_tiles(const ProductArgs& a)
-{
-    uint32_t sum = 0;
-    for (uint32_t e = lane_id(); e < a.experts; e += 64) {
-        uint32_t begin, end;
-        expert_rows(a, e, begin, end);
-        sum += (end - begin + kRows - 1) / kRows;
-    }
-    for (uint32_t d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
-    return __builtin_amdgcn_readfirstlane(sum);
-}
+struct RowTiles {
+    uint32_t begin, end, tiles, sum;   // of expert `lane` of the 64 at hand; sum: running, over lanes
 
-// The expert and the rows of row tile `tile`, tiles of kRows rows counted expert after
-// expert.  Every wave looks for itself: 64 experts at a time, a running sum over lanes.
-// False past the last tile.
-template <uint32_t kRows>
-__device__ inline bool find_tile(const ProductArgs& a, uint32_t tile, uint32_t& expert, uint32_t& row0, uint32_t& rows)
-{
-    const uint32_t lane = lane_id();
-    uint32_t before = 0;
-    for (uint32_t e0 = 0; e0 < a.experts; e0 += 64) {
-        uint32_t begin = 0, end = 0;
-        if (e0 + lane < a.experts) expert_rows(a, e0 + lane, begin, end);
-        const uint32_t tiles = (end - begin + kRows - 1) / kRows;
-        uint32_t sum = tiles;
+    __device__ inline void look(const ProductArgs& a, uint32_t e0)
+    {
+        begin = end = 0;
+        if (e0 + lane_id() < a.experts) expert_rows(a, e0 + lane_id(), begin, end);
+        sum = tiles = (end - begin + kRows - 1) / kRows;
         for (uint32_t d = 1; d < 64; d <<= 1) {
             const uint32_t up = __shfl_up(sum, d);
-            if (lane >= d) sum += up;
+            if (lane_id() >= d) sum += up;
         }
-        const uint64_t past = __ballot(before + sum > tile);
-        if (past) {
-            const int l = __builtin_ctzll(past);
-            const uint32_t at = tile - (before + __shfl(sum, l) - __shfl(tiles, l));
-            const uint32_t b = __shfl(begin, l), e = __shfl(end, l);
-            expert = __builtin_amdgcn_readfirstlane(e0 + uint32_t(l));
-            row0 = __builtin_amdgcn_readfirstlane(b + at * kRows);
-            rows = __builtin_amdgcn_readfirstlane(min(kRows, e - row0));
-            return true;
-        }
-        before += __shfl(sum, 63);
     }
-    return false;
-}
 
-// 8 consecutive outputs from n on: sums of a row scaled, rounded and stored.
+    __device__ inline RowTiles(const ProductArgs& a) { look(a, 0); }
+
+    __device__ inline uint32_t here() const { return __builtin_amdgcn_readlane(sum, 63); }
+
+    // Tiles of all experts.
+    __device__ inline uint32_t count(const ProductArgs& a)
+    {
+        uint32_t n = here();
+        for (uint32_t e0 = 64; e0 < a.experts; e0 += 64) {
+            look(a, e0);
+            n += here();
+        }
+        if (a.experts > 64) look(a, 0);
+        return n;
+    }
+
+    // Expert and rows of tile `tile`; false past the last.
+    __device__ inline bool find(const ProductArgs& a, uint32_t tile, uint32_t& expert, uint32_t& row0, uint32_t& rows)
+    {
+        uint32_t before = 0;
+        for (uint32_t e0 = 0;;) {
+            const uint64_t past = __ballot(before + sum > tile);
+            if (past) {
+                const uint32_t l = uint32_t(__builtin_ctzll(past));
+                const uint32_t at = tile - before - (__builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(tiles, l));
+                expert = e0 + l;
+                row0 = __builtin_amdgcn_readlane(begin, l) + at * kRows;
+                rows = min(kRows, __builtin_amdgcn_readlane(end, l) - row0);
+                return true;
+            }
+            before += here();
+            e0 += 64;
+            if (e0 >= a.experts) return false;
+            look(a, e0);
+        }
+    }
+};
+
+// 8 consecutive outputs from n on: a row's scaled sums times the weights' scales, rounded
+// and stored.
 struct Outputs {
     float ws[8];
     uint32_t n, count;
@@ -199,13 +211,13 @@ struct Outputs {
         for (uint32_t r = 0; r < 8; r++) ws[r] = r < count ? from[r] : 0.0f;
     }
 
-    __device__ inline void store(const ProductArgs& a, uint32_t row, v4i lo, v4i hi) const
+    // v: sum * row scale
+    __device__ inline void store(const ProductArgs& a, uint32_t row, v4f lo, v4f hi) const
     {
-        const float scale = a.scales[row];
         const uint64_t at = uint64_t(row) * a.out_stride + n;
         float f[8];
 #pragma unroll
-        for (uint32_t r = 0; r < 8; r++) f[r] = float(r < 4 ? lo[r & 3] : hi[r & 3]) * scale * ws[r];
+        for (uint32_t r = 0; r < 8; r++) f[r] = (r < 4 ? lo[r & 3] : hi[r & 3]) * ws[r];
         if (a.fp32) {
             float* o = reinterpret_cast<float*>(a.out) + at;
             if (count == 8) {
@@ -231,13 +243,16 @@ struct Outputs {
     }
 };
 
-// All waves: n loads may still be in flight (the oldest have landed), no LDS read is, and
-// nothing moves across.
+// All waves: n loads may still be in flight (the older ones have landed), no LDS read is,
+// and nothing moves across.
 template <uint32_t N>
 __device__ inline void wait_loads_and_meet()
 {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
+
+// All waves: no LDS read is in flight.
+__device__ inline void wait_reads_and_meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 typedef __attribute__((address_space(1))) const void global_void;
 typedef __attribute__((address_space(3))) void lds_void;
@@ -248,123 +263,126 @@ __device__ inline void load_lds(const int8_t* from, uint8_t* to)
     __builtin_amdgcn_global_load_lds((global_void*)from, (lds_void*)to, 16, 0, 0);
 }
 
-// The share of the tiles this workgroup takes.  Workgroups go to the 8 XCDs in turn; each
-// XCD takes a run of consecutive tiles, and tiles run over kBand row tiles, then over the
-// outputs, so that those an XCD works on at one time share rows and weights in its L2.
-constexpr uint32_t kXcds = 8, kBand = 4;
-
-template <uint32_t kRows>
-__device__ inline bool take_tile(const ProductArgs& a, uint32_t across, uint32_t& expert, uint32_t& row0,
-                                 uint32_t& rows, uint32_t& column)
+// Order of issue: `kProducts` matrix instructions and kOthers of one kind (0x100 LDS
+// reads, 0x020 loads) taking turns.
+template <int kProducts, int kOthers, int kKind, int kAt = 0>
+__device__ inline void take_turns()
 {
-    const uint32_t down = count_tiles<kRows>(a), total = down * across;
-    const uint32_t per = (total + kXcds - 1) / kXcds;
-    const uint32_t at = blockIdx.x / kXcds, t = blockIdx.x % kXcds * per + at;
-    if (at >= per || t >= total) return false;
-    const uint32_t band = t / (kBand * across), in = t % (kBand * across);
-    const uint32_t high = min(kBand, down - band * kBand);
-    column = in / high;
-    return find_tile<kRows>(a, band * kBand + in % high, expert, row0, rows);
+    if constexpr (kAt < kOthers) {
+        constexpr int n = (kAt + 1) * kProducts / kOthers - kAt * kProducts / kOthers;
+        if constexpr (n > 0) __builtin_amdgcn_sched_group_barrier(0x008, n, 0);
+        __builtin_amdgcn_sched_group_barrier(kKind, 1, 0);
+        take_turns<kProducts, kOthers, kKind, kAt + 1>();
+    }
 }
 
-// A tile of 64 kM rows x 64 kN outputs per workgroup of 4 waves, each 32 kM x 32 kN.  The
-// rows go through LDS in steps of 64 values, four steps deep: step h + 4 is requested
-// into the place of step h once every wave holds step h in registers, and while a wave
-// multiplies step h it reads step h + 1 from LDS.  One barrier per step.
 constexpr uint32_t kTileThreads = 256;
-constexpr uint32_t kStep = 64, kStages = 4;
+constexpr uint32_t kSlab = kQuantPad;   // values of a row per step
 
-template <uint32_t kM, uint32_t kN>
-__global__ __launch_bounds__(kTileThreads, kM * kN > 8 ? 1 : 2) void product_tile_kernel(const ProductArgs a)
+// LDS of a tile of 64 kM rows x 64 kN outputs.
+constexpr uint32_t slot_bytes(uint32_t m, uint32_t n) { return 64 * (m + n) * kSlab; }
+constexpr uint32_t tile_lds(uint32_t m, uint32_t n, uint32_t slots) { return slots * slot_bytes(m, n); }
+
+// A tile of up to 64 kM rows x 64 kN outputs by 4 waves, each 32 kM x 32 kN.
+//
+// The rows go through LDS in slabs of 128 values (whole 128-byte lines: requests of 64
+// bytes kept the L2's channels busy twice as long), kSlots slabs in a ring.  A wave holds
+// the first half of slab s in registers when the step begins.  It reads the second half
+// while it multiplies the first; then, slab s being free, it requests slab s + kSlots
+// into its place while it multiplies on, and, slab s + 1 having landed, reads that one's
+// first half.  Loads are issued one per two matrix instructions: a wave's load keeps the
+// CU's address path busy for 16 cycles, a matrix instruction its SIMD for 32, and at one
+// load per instruction of each of the four waves the loads held the products up
+// (256 x 256 x 7168, zeros: 3540 TOP/s at one per product, 4030 at one per two).
+template <uint32_t kM, uint32_t kN, uint32_t kSlots>
+__device__ inline void product_tile(const ProductArgs& a, uint8_t* s_ring, uint32_t expert, uint32_t row0,
+                                    uint32_t rows, uint32_t n0)
 {
-    constexpr uint32_t kRows = 64 * kM, kOuts = 64 * kN;
-    constexpr uint32_t kStage = (kRows + kOuts) * kStep, kLoads = kM + kN;   // bytes, loads per thread of a step
-    // LDS reads go between the first half of a step's products, loads between the second
-    constexpr uint32_t kHalf = kM * kN;
-    constexpr uint32_t kReadEach = (2 * kLoads + kHalf - 1) / kHalf, kLoadEach = kHalf > kLoads ? kHalf / kLoads : 1;
-    extern __shared__ __attribute__((aligned(1024))) uint8_t s_stage[];
-    const uint32_t across = (a.outputs + kOuts - 1) / kOuts;
-    uint32_t expert, row0, rows, column;
-    if (!take_tile<kRows>(a, across, expert, row0, rows, column)) return;
-    const uint32_t n0 = column * kOuts;
+    constexpr uint32_t kRows = 64 * kM, kSlot = slot_bytes(kM, kN);
+    constexpr uint32_t kLoads = 2 * (kM + kN), kEarly = kLoads / 2;   // loads of a thread per slab
+    constexpr uint32_t kProducts = kM * kN;                           // products of a quarter slab
     const uint32_t lane = lane_id();
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int8_t* q = a.q + uint64_t(row0) * a.q_stride;
     const int8_t* w = a.w + (uint64_t(expert) * a.outputs + n0) * a.w_stride;
 
-    // A load of a wave fills 16 rows of 64 bytes.  The 16-byte pieces of a row are
-    // swapped by bits 2-3 of the row so that 16 lanes reading one piece of 16 rows use
-    // every bank.  Rows past the tile's end repeat its last one and are not stored.
-    const int8_t* from[kLoads];
-    const uint32_t r = 16 * wave + lane / 4, piece = (lane & 3) ^ ((lane >> 4) & 3);
+    // A load of a wave fills 8 rows of 128 bytes.  The 16-byte pieces of a row are swapped
+    // by bits 1-3 of the row, so that 16 lanes reading one piece of 16 rows use every
+    // bank.  Rows past the tile's end repeat its last one and are not stored.
+    uint32_t from[kLoads];
+    const uint32_t r = 8 * wave + lane / 8, piece = (lane & 7) ^ ((r >> 1) & 7);
 #pragma unroll
     for (uint32_t i = 0; i < kLoads; i++)
-        from[i] = (i < kM ? a.q + uint64_t(row0 + min(r + 64 * i, rows - 1)) * a.q_stride
-                          : w + uint64_t(min(r + 64 * (i - kM), a.outputs - 1 - n0)) * a.w_stride) + 16 * piece;
-    const uint32_t steps = 2 * a.slabs;
-    const auto load = [&](uint32_t step) {
-        const uint32_t at = min(step, steps - 1) * kStep;   // past the end: the last step again, never used
-        uint8_t* to = s_stage + (step % kStages) * kStage + 1024 * wave;
+        from[i] = (i < 2 * kM ? min(r + 32 * i, rows - 1) * uint32_t(a.q_stride)
+                              : min(r + 32 * (i - 2 * kM), a.outputs - 1 - n0) * uint32_t(a.w_stride)) + 16 * piece;
+    const auto load = [&](uint32_t slab, uint32_t first, uint32_t end) {
+        const uint32_t at = min(slab, a.slabs - 1) * kSlab;   // past the end: the last slab again, never used
+        uint8_t* to = s_ring + slab % kSlots * kSlot + 1024 * wave;
 #pragma unroll
-        for (uint32_t i = 0; i < kLoads; i++) load_lds(from[i] + at, to + 4096 * i);
+        for (uint32_t i = first; i < end; i++) load_lds((i < 2 * kM ? q : w) + at + from[i], to + 4096 * i);
     };
 
     const uint32_t wm = (wave >> 1) * 32 * kM, wn = (wave & 1) * 32 * kN;
-    const uint32_t half = lane >> 5, turn = (lane >> 2) & 3;
-    const uint8_t* read_q = s_stage + (wm + (lane & 31)) * kStep;
-    const uint8_t* read_w = s_stage + (kRows + wn + (lane & 31)) * kStep;
+    const uint32_t half = lane >> 5, turn = (lane >> 1) & 7;
+    const uint8_t* read_q = s_ring + (wm + (lane & 31)) * kSlab;
+    const uint8_t* read_w = s_ring + (kRows + wn + (lane & 31)) * kSlab;
     v16i acc[kM][kN] = {};
     v4i fq[2][2][kM], fw[2][2][kN];
-    const auto read = [&](uint32_t to, uint32_t step) {
-        const uint32_t base = (step % kStages) * kStage;
+    const auto read = [&](uint32_t to, uint32_t slab) {   // half `to` of a slab into registers `to`
+        const uint32_t slot = slab % kSlots * kSlot;
 #pragma unroll
         for (uint32_t k = 0; k < 2; k++) {
-            const uint32_t at = base + ((2 * k + half) ^ turn) * 16;
+            const uint32_t at = slot + ((4 * to + 2 * k + half) ^ turn) * 16;
 #pragma unroll
-            for (uint32_t i = 0; i < kM; i++) fq[to][k][i] = *reinterpret_cast<const v4i*>(read_q + at + 32 * kStep * i);
+            for (uint32_t i = 0; i < kM; i++) fq[to][k][i] = *reinterpret_cast<const v4i*>(read_q + at + 32 * kSlab * i);
 #pragma unroll
-            for (uint32_t j = 0; j < kN; j++) fw[to][k][j] = *reinterpret_cast<const v4i*>(read_w + at + 32 * kStep * j);
+            for (uint32_t j = 0; j < kN; j++) fw[to][k][j] = *reinterpret_cast<const v4i*>(read_w + at + 32 * kSlab * j);
         }
     };
-
-    for (uint32_t h = 0; h < kStages; h++) load(h);
-    wait_loads_and_meet<(kStages - 1) * kLoads>();
+    const auto multiply = [&](uint32_t u, uint32_t k) {
+#pragma unroll
+        for (uint32_t i = 0; i < kM; i++)
+#pragma unroll
+            for (uint32_t j = 0; j < kN; j++)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[u][k][j], fq[u][k][i], acc[i][j], 0, 0, 0);
+    };
+#pragma unroll
+    for (uint32_t s = 0; s < kSlots; s++) load(s, 0, kLoads);
+    wait_loads_and_meet<(kSlots - 1) * kLoads>();
     read(0, 0);
-    for (uint32_t h0 = 0; h0 < steps; h0 += 2) {
-#pragma unroll
-        for (uint32_t u = 0; u < 2; u++) {
-            wait_loads_and_meet<(kStages - 2) * kLoads>();
-            read(u ^ 1, h0 + u + 1);
-            load(h0 + u + kStages);
-#pragma unroll
-            for (uint32_t k = 0; k < 2; k++)
-#pragma unroll
-                for (uint32_t i = 0; i < kM; i++)
-#pragma unroll
-                    for (uint32_t j = 0; j < kN; j++)
-                        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[u][k][j], fq[u][k][i], acc[i][j], 0, 0, 0);
-#pragma unroll
-            for (uint32_t g = 0; g < kHalf; g++) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x100, kReadEach, 0);
-            }
-#pragma unroll
-            for (uint32_t g = 0; g < kLoads; g++) {
-                __builtin_amdgcn_sched_group_barrier(0x008, kLoadEach, 0);
-                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        }
+    for (uint32_t s = 0; s < a.slabs; s++) {
+        read(1, s);
+        multiply(0, 0);
+        take_turns<kProducts / 2 + 1, kLoads, 0x100>();
+        __builtin_amdgcn_sched_barrier(0);
+        wait_reads_and_meet();
+        load(s + kSlots, 0, kEarly);
+        multiply(0, 1);
+        take_turns<kProducts, kEarly, 0x020>();
+        __builtin_amdgcn_sched_barrier(0);
+        wait_loads_and_meet<(kSlots - 2) * kLoads + kEarly>();
+        load(s + kSlots, kEarly, kLoads);
+        read(0, s + 1);
+        multiply(1, 0);
+        multiply(1, 1);
+        take_turns<kProducts, kLoads - kEarly, 0x020>();
+        take_turns<kProducts / 2 + 1, kLoads, 0x100>();
+        __builtin_amdgcn_sched_barrier(0);
     }
-    wait_loads_and_meet<0>();   // the surplus loads have landed: LDS is free
 
     // Lane l holds, of each 32 x 32 piece, row l % 32 and outputs 8 g + 4 (l / 32) .. + 3.
     // Strips of 32 rows change hands in the wave's own part of LDS so that a lane gets 8
     // outputs in a row and a store covers whole rows of the wave's outputs.
     constexpr uint32_t kPitch = 32 * kN * 4 + 16;       // bytes; the 16 spread rows over the banks
     constexpr uint32_t kPerRow = 4 * kN;                // lanes of a row
-    uint8_t* strip = s_stage + wave * (32 * kPitch);
+    static_assert(4 * 32 * kPitch <= kSlots * kSlot, "strips fit the ring");
+    float scale[kM];
+#pragma unroll
+    for (uint32_t i = 0; i < kM; i++) scale[i] = a.scales[row0 + min(wm + 32 * i + (lane & 31), rows - 1)];
     const uint32_t n = n0 + wn + 8 * (lane % kPerRow);
     const Outputs to(a, expert, n);
+    wait_loads_and_meet<0>();   // the surplus loads have landed and every wave is done reading: the ring is free
+    uint8_t* strip = s_ring + wave * (32 * kPitch);
 #pragma unroll
     for (uint32_t i = 0; i < kM; i++) {
         if (wm + 32 * i >= rows) break;
@@ -372,19 +390,53 @@ __global__ __launch_bounds__(kTileThreads, kM * kN > 8 ? 1 : 2) void product_til
         for (uint32_t j = 0; j < kN; j++)
 #pragma unroll
             for (uint32_t g = 0; g < 4; g++) {
-                const v4i v = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
-                *reinterpret_cast<v4i*>(strip + (lane & 31) * kPitch + (32 * j + 8 * g + 4 * half) * 4) = v;
+                const v4f v = {float(acc[i][j][4 * g]) * scale[i], float(acc[i][j][4 * g + 1]) * scale[i],
+                               float(acc[i][j][4 * g + 2]) * scale[i], float(acc[i][j][4 * g + 3]) * scale[i]};
+                *reinterpret_cast<v4f*>(strip + (lane & 31) * kPitch + (32 * j + 8 * g + 4 * half) * 4) = v;
             }
         __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
+#pragma unroll 2
         for (uint32_t at = lane / kPerRow; at < 32; at += 64 / kPerRow) {
             const uint32_t row = wm + 32 * i + at;
             if (row >= rows) break;
-            const v4i* v = reinterpret_cast<const v4i*>(strip + at * kPitch + 32 * (lane % kPerRow));
+            const v4f* v = reinterpret_cast<const v4f*>(strip + at * kPitch + 32 * (lane % kPerRow));
             to.store(a, row0 + row, v[0], v[1]);
         }
         __builtin_amdgcn_wave_barrier();
     }
+}
+
+// Workgroups go to the 8 XCDs in turn; each XCD takes a run of consecutive tiles, and
+// tiles run over kBand row tiles, then over the outputs, so that those an XCD works on at
+// one time share rows and weights in its L2.
+constexpr uint32_t kXcds = 8, kBand = 4;
+
+__device__ inline uint32_t run_of_xcd(uint32_t id, uint32_t total)
+{
+    const uint32_t per = (total + kXcds - 1) / kXcds;
+    return id / kXcds < per ? min(id % kXcds * per + id / kXcds, total) : total;
+}
+
+__device__ inline void tile_at(uint32_t t, uint32_t down, uint32_t across, uint32_t& row_tile, uint32_t& column)
+{
+    const uint32_t band = t / (kBand * across), in = t % (kBand * across);
+    const uint32_t high = min(kBand, down - band * kBand);
+    row_tile = band * kBand + in % high;
+    column = in / high;
+}
+
+template <uint32_t kM, uint32_t kN, uint32_t kSlots, uint32_t kPerCu>
+__global__ __launch_bounds__(kTileThreads, kPerCu) void product_tile_kernel(const ProductArgs a)
+{
+    extern __shared__ __attribute__((aligned(1024))) uint8_t s_ring[];
+    RowTiles<64 * kM> map(a);
+    const uint32_t across = (a.outputs + 64 * kN - 1) / (64 * kN), down = map.count(a);
+    const uint32_t t = run_of_xcd(blockIdx.x, down * across);
+    if (t >= down * across) return;
+    uint32_t row_tile, column, expert, row0, rows;
+    tile_at(t, down, across, row_tile, column);
+    if (!map.find(a, row_tile, expert, row0, rows)) return;
+    product_tile<kM, kN, kSlots>(a, s_ring, expert, row0, rows, 64 * kN * column);
 }
 
 // Row tiles that any split of `rows` rows over the experts can need.
@@ -405,20 +457,16 @@ hipError_t launch_quantize_rows(const QuantArgs& a, hipStream_t s)
 
 namespace {
 
-// Tile shapes (in units of 64 x 64).
-constexpr uint32_t kLargeM = 4, kLargeN = 4;
-constexpr uint32_t kSmallM = 2, kSmallN = 2;
-
 uint64_t tile_workgroups(const ProductArgs& a, uint32_t m, uint32_t n)
 {
     return (most_tiles(a, 64 * m) * ((a.outputs + 64 * n - 1) / (64 * n)) + kXcds - 1) / kXcds * kXcds;
 }
 
-template <uint32_t kM, uint32_t kN>
+template <uint32_t kM, uint32_t kN, uint32_t kSlots, uint32_t kPerCu>
 hipError_t launch_tiles(const ProductArgs& a, hipStream_t s)
 {
-    constexpr uint32_t lds = kStages * 64 * (kM + kN) * kStep;
-    const auto kernel = product_tile_kernel<kM, kN>;
+    constexpr uint32_t lds = tile_lds(kM, kN, kSlots);
+    const auto kernel = product_tile_kernel<kM, kN, kSlots, kPerCu>;
     if (lds > 65536) {
         if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                                hipFuncAttributeMaxDynamicSharedMemorySize, int(lds)))
@@ -428,18 +476,27 @@ hipError_t launch_tiles(const ProductArgs& a, hipStream_t s)
     return hipGetLastError();
 }
 
-bool use_large(const ProductArgs& a) { return tile_workgroups(a, kLargeM, kLargeN) >= 256; }
+bool use_large(const ProductArgs& a) { return tile_workgroups(a, 4, 4) >= 256; }
 
 }  // namespace
 
 uint64_t product_workgroups(const ProductArgs& a)
 {
-    return use_large(a) ? tile_workgroups(a, kLargeM, kLargeN) : tile_workgroups(a, kSmallM, kSmallN);
+    return use_large(a) ? tile_workgroups(a, 4, 4) : tile_workgroups(a, 2, 2);
 }
 
 hipError_t launch_experts_product(const ProductArgs& a, hipStream_t s)
 {
-    return use_large(a) ? launch_tiles<kLargeM, kLargeN>(a, s) : launch_tiles<kSmallM, kSmallN>(a, s);
+    const char* v = getenv("ZV");
+    if (v && *v == 'a') return launch_tiles<1, 2, 2, 3>(a, s);
+    if (v && *v == 'b') return launch_tiles<1, 2, 4, 1>(a, s);
+    if (v && *v == 'c') return launch_tiles<2, 2, 2, 2>(a, s);
+    if (v && *v == 'd') return launch_tiles<2, 2, 4, 1>(a, s);
+    if (v && *v == 'e') return launch_tiles<1, 1, 2, 4>(a, s);
+    if (v && *v == 'f') return launch_tiles<1, 1, 4, 2>(a, s);
+    if (v && *v == 'g') return launch_tiles<4, 4, 2, 1>(a, s);
+    if (v && *v == 'h') return launch_tiles<1, 2, 3, 2>(a, s);
+    return use_large(a) ? launch_tiles<4, 4, 2, 1>(a, s) : launch_tiles<2, 2, 2, 2>(a, s);
 }
 
 }  // namespace zc

@@ -21,6 +21,7 @@ constexpr uint64_t kMaxCount = 1ull << 31;     // choices, rows: 32-bit signed i
 constexpr uint64_t kMaxRowLen = 1ull << 28;
 constexpr uint64_t kMaxSumLen = 131071;        // 128 * 128 * this stays below 2^31
 constexpr uint64_t kMaxTiles = 1ull << 24;     // workgroups of one launch
+constexpr uint64_t kMaxByteStride = 1ull << 24;  // of the product's rows: 255 of them stay within 32 bits
 constexpr uint64_t kMaxStride = 1ull << 40;    // keeps row index * stride * 4 within 64 bits
 
 bool is_dtype(int d) { return d == ZIPCCL_BF16 || d == ZIPCCL_FP32; }
@@ -228,8 +229,8 @@ zipccl_status zipccl_experts_product(const void* q, uint64_t q_stride, const flo
     if (!offsets && num_experts != 1) return ZIPCCL_ERR_INVALID;
     if (!w || !w_scales || (rows > 0 && (!q || !scales))) return ZIPCCL_ERR_INVALID;
     if (q_stride < row_len || w_stride < row_len) return ZIPCCL_ERR_INVALID;
-    if (rows >= kMaxCount || row_len > kMaxSumLen || outputs >= (1ull << 24) || q_stride >= kMaxStride ||
-        w_stride >= kMaxStride)
+    if (rows >= kMaxCount || row_len > kMaxSumLen || outputs >= (1ull << 24) || q_stride > kMaxByteStride ||
+        w_stride > kMaxByteStride)
         return ZIPCCL_ERR_SIZE;
     if (q_stride % kQuantPad != 0 || w_stride % kQuantPad != 0 || !aligned(q, 16) || !aligned(w, 16) ||
         !aligned(scales, 4) || !aligned(w_scales, 4) || !aligned(offsets, 4) || (status && !aligned(status, 4)))
