@@ -427,7 +427,7 @@ typedef enum zipccl_dtype { ZIPCCL_BF16 = 0, ZIPCCL_FP32 = 1 } zipccl_dtype;
  *   slots       device int32[tokens * top_k]
  *   workspace   device scratch, 256-byte aligned, ZIPCCL_MOE_SORT_WORKSPACE_BYTES; carries
  *               nothing between calls; concurrent calls need separate ones
- * One launch up to 16384 choices, two above.
+ * One launch up to 2048 choices, two above.
  * Errors: INVALID (NULL pointers, top_k outside 1..ZIPCCL_MAX_TOP_K, num_experts outside
  * 1..ZIPCCL_MAX_EXPERTS, id_bytes, stride < top_k), ALIGN, SIZE, HIP. */
 zipccl_status zipccl_moe_sort(const void* experts, int id_bytes, uint64_t stride, uint64_t tokens, int top_k,

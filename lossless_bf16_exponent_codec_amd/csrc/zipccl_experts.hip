@@ -439,6 +439,33 @@ __global__ __launch_bounds__(kTileThreads, kPerCu) void product_tile_kernel(cons
     product_tile<kM, kN, kSlots>(a, s_ring, expert, row0, rows, 64 * kN * column);
 }
 
+// Tiles of 256 x 256, one workgroup per CU.  Where the tiles past the last whole round of
+// the 256 CUs are few, each is cut into four of 128 x 128, so that the last round takes a
+// part of a tile's time.
+constexpr uint32_t kCus = 256, kCutTiles = kCus / 4;
+
+__global__ __launch_bounds__(kTileThreads, 1) void product_large_kernel(const ProductArgs a)
+{
+    extern __shared__ __attribute__((aligned(1024))) uint8_t s_ring[];
+    RowTiles<256> map(a);
+    const uint32_t across = (a.outputs + 255) / 256, down = map.count(a), total = down * across;
+    const uint32_t left = total % kCus;
+    const uint32_t whole = left <= kCutTiles ? total - left : total;   // the tiles not cut
+    const bool cut = blockIdx.x >= whole;
+    const uint32_t parts = 4 * (total - whole);
+    const uint32_t p = cut ? run_of_xcd(blockIdx.x - whole, parts) : run_of_xcd(blockIdx.x, whole);
+    if (p >= (cut ? parts : whole)) return;
+    uint32_t row_tile, column, expert, row0, rows;
+    tile_at(cut ? whole + p / 4 : p, down, across, row_tile, column);
+    if (!map.find(a, row_tile, expert, row0, rows)) return;
+    if (!cut) {
+        product_tile<4, 4, 2>(a, s_ring, expert, row0, rows, 256 * column);
+        return;
+    }
+    const uint32_t r = 128 * (p & 1), n0 = 256 * column + 64 * (p & 2);
+    if (r < rows && n0 < a.outputs) product_tile<2, 2, 2>(a, s_ring, expert, row0 + r, min(rows - r, 128u), n0);
+}
+
 // Row tiles that any split of `rows` rows over the experts can need.
 uint64_t most_tiles(const ProductArgs& a, uint32_t per_tile)
 {
@@ -476,13 +503,26 @@ hipError_t launch_tiles(const ProductArgs& a, hipStream_t s)
     return hipGetLastError();
 }
 
+// most_tiles bounds the whole tiles; cutting the last ones adds 3 workgroups for each
+uint64_t large_workgroups(const ProductArgs& a) { return tile_workgroups(a, 4, 4) + 3 * kCutTiles; }
+
+hipError_t launch_large(const ProductArgs& a, hipStream_t s)
+{
+    constexpr uint32_t lds = tile_lds(4, 4, 2);
+    if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(product_large_kernel),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, int(lds)))
+        return e;
+    hipLaunchKernelGGL(product_large_kernel, dim3(uint32_t(large_workgroups(a))), dim3(kTileThreads), lds, s, a);
+    return hipGetLastError();
+}
+
 bool use_large(const ProductArgs& a) { return tile_workgroups(a, 4, 4) >= 256; }
 
 }  // namespace
 
 uint64_t product_workgroups(const ProductArgs& a)
 {
-    return use_large(a) ? tile_workgroups(a, 4, 4) : tile_workgroups(a, 2, 2);
+    return use_large(a) ? large_workgroups(a) : tile_workgroups(a, 2, 2);
 }
 
 hipError_t launch_experts_product(const ProductArgs& a, hipStream_t s)
@@ -494,9 +534,10 @@ hipError_t launch_experts_product(const ProductArgs& a, hipStream_t s)
     if (v && *v == 'd') return launch_tiles<2, 2, 4, 1>(a, s);
     if (v && *v == 'e') return launch_tiles<1, 1, 2, 4>(a, s);
     if (v && *v == 'f') return launch_tiles<1, 1, 4, 2>(a, s);
-    if (v && *v == 'g') return launch_tiles<4, 4, 2, 1>(a, s);
-    if (v && *v == 'h') return launch_tiles<1, 2, 3, 2>(a, s);
-    return use_large(a) ? launch_tiles<4, 4, 2, 1>(a, s) : launch_tiles<2, 2, 2, 2>(a, s);
+    if (v && *v == 'g') return launch_large(a, s);
+    if (v && *v == 'h') return launch_tiles<4, 2, 2, 1>(a, s);
+    if (v && *v == 'i') return launch_tiles<2, 4, 2, 1>(a, s);
+    return use_large(a) ? launch_large(a, s) : launch_tiles<2, 2, 2, 2>(a, s);
 }
 
 }  // namespace zc

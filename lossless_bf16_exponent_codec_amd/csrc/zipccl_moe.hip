@@ -14,6 +14,8 @@ namespace zc {
 
 namespace {
 
+template <uint32_t N> struct Constant { static constexpr uint32_t value = N; };
+
 __device__ inline uint32_t lane_id() { return __lane_id(); }
 
 __device__ inline void set_status(uint32_t* status, uint32_t bits)
@@ -27,9 +29,13 @@ __device__ inline void set_status(uint32_t* status, uint32_t bits)
 // A stable counting sort of n = tokens * top_k choices: slot(i) = (choices of smaller
 // experts) + (earlier choices of the same expert).  Each workgroup takes a consecutive
 // share of the choices and each of its waves a consecutive part of that share, so
-// "earlier" splits into earlier workgroups (counts in the workspace), earlier waves
-// (counts in LDS) and earlier lanes or groups of the wave (ballots).  One workgroup
-// needs no counts from others: small calls are one launch.
+// "earlier" splits into earlier workgroups (counts in the workspace), earlier waves and
+// earlier groups of 64 of the wave (counts in LDS), and earlier lanes (ballots).  One
+// workgroup needs no counts from others: small calls are one launch.
+//
+// Nothing here is bound by bandwidth (2 MB for 131072 choices); what counts is the chain
+// of dependent steps.  A wave therefore ranks its choices once, holds the ranks in
+// registers across the scan over experts, and adds the expert's base after it.
 // ------------------------------------------------------------------------------------
 __device__ inline int32_t load_id(const SortArgs& a, uint32_t i, bool& bad)
 {
@@ -42,12 +48,21 @@ __device__ inline int32_t load_id(const SortArgs& a, uint32_t i, bool& bad)
     return id < 0 ? -1 : int32_t(id);
 }
 
+// Neighbouring shares go to one XCD (workgroups go to the 8 XCDs in turn), where the
+// pieces of a line of `rows` that they write meet in one L2.
+__device__ inline uint32_t sort_block(const SortArgs& a)
+{
+    return a.blocks > 1 ? blockIdx.x % 8 * ((a.blocks + 7) / 8) + blockIdx.x / 8 : 0;
+}
+
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const SortArgs a)
 {
+    const uint32_t block = sort_block(a);
+    if (block >= a.blocks) return;
     __shared__ uint32_t s_count[kMaxExperts];
     for (uint32_t e = threadIdx.x; e < a.experts; e += kSortThreads) s_count[e] = 0;
     __syncthreads();
-    const uint32_t first = blockIdx.x * a.per_block, end = min(a.n, first + a.per_block);
+    const uint32_t first = block * a.per_block, end = min(a.n, first + a.per_block);
     bool bad = false;
     for (uint32_t i = first + threadIdx.x; i < end; i += kSortThreads) {
         const int32_t id = load_id(a, i, bad);
@@ -55,43 +70,105 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const SortArgs
     }
     __syncthreads();
     for (uint32_t e = threadIdx.x; e < a.experts; e += kSortThreads)
-        a.hist[uint64_t(blockIdx.x) * a.experts + e] = s_count[e];
+        a.hist[uint64_t(block) * a.experts + e] = s_count[e];
 }
 
+// kGroups: groups of 64 choices per wave held in registers; 0: any number, ranked twice.
+template <uint32_t kGroups>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const SortArgs a)
 {
-    extern __shared__ uint32_t s_next[];            // [wave][expert]: counts, then the next slot
+    const uint32_t block = sort_block(a);
+    if (block >= a.blocks) return;
+    extern __shared__ uint32_t s_next[];            // [wave][expert]: choices so far, then the expert's base
     __shared__ uint32_t s_wave_sum[kSortWaves];
+    __shared__ uint32_t s_before[kSortThreads], s_all[kSortThreads];
     const uint32_t tid = threadIdx.x, lane = lane_id();
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t E = a.experts;
+    const uint32_t per_wave = kGroups ? 64 * kGroups : a.per_block / kSortWaves;
+    const uint32_t first = block * a.per_block + wave * per_wave, end = min(a.n, first + per_wave);
+    uint32_t* next = s_next + wave * E;
+    constexpr uint32_t kHeld = kGroups ? kGroups : 1;
+    int32_t id[kHeld];
+    bool bad = false;
+    if constexpr (kGroups > 0) {
+#pragma unroll
+        for (uint32_t g = 0; g < kGroups; g++) {
+            const uint32_t i = first + 64 * g + lane;
+            id[g] = i < end ? load_id(a, i, bad) : -1;
+        }
+    }
+    // the other workgroups' counts: threads share an expert's blocks where there are
+    // more threads than experts
+    if (a.blocks > 1) {
+        const uint32_t shares = kSortThreads / E, e = tid % E, share = tid / E;
+        uint32_t before = 0, all = 0;
+        const auto gather = [&](auto batch) {   // loads in flight
+            constexpr uint32_t kBatch = decltype(batch)::value;
+            for (uint32_t b0 = 0; b0 < a.blocks; b0 += kBatch * shares) {
+                uint32_t c[kBatch];
+#pragma unroll
+                for (uint32_t j = 0; j < kBatch; j++) c[j] = a.hist[min(b0 + j * shares + share, a.blocks - 1) * E + e];
+#pragma unroll
+                for (uint32_t j = 0; j < kBatch; j++) {
+                    const uint32_t b = b0 + j * shares + share;
+                    all += b < a.blocks ? c[j] : 0;
+                    before += b < block ? c[j] : 0;
+                }
+            }
+        };
+        if (a.blocks > 4 * shares) gather(Constant<16>());
+        else gather(Constant<4>());
+        if (share >= shares) before = all = 0;   // threads past the last whole share
+        s_before[tid] = before;
+        s_all[tid] = all;
+    }
     for (uint32_t j = tid; j < kSortWaves * E; j += kSortThreads) s_next[j] = 0;
     __syncthreads();
 
-    const uint32_t block_first = blockIdx.x * a.per_block;
-    const uint32_t per_wave = a.per_block / kSortWaves;
-    const uint32_t first = block_first + wave * per_wave, end = min(a.n, first + per_wave);
-    uint32_t* next = s_next + wave * E;
-    bool bad = false;
-    for (uint32_t i = first + lane; i < end; i += 64) {
-        const int32_t id = load_id(a, i, bad);
-        if (id >= 0) atomicAdd(&next[id], 1u);
+    // Lanes of one expert in a group of 64 find each other by ballots over the bits of
+    // its number.  Returns how many earlier choices of the wave have the lane's expert;
+    // the first lane of each expert moves the wave's counter on.
+    const uint32_t bits = E > 1 ? 32 - __builtin_clz(E - 1) : 0;
+    const auto rank = [&](int32_t of) {
+        uint64_t same = __ballot(of >= 0);
+        for (uint32_t b = 0; b < bits; b++) {
+            const bool on = (of >> b) & 1;
+            const uint64_t m = __ballot(on);
+            same &= on ? m : ~m;
+        }
+        uint32_t at = 0;
+        if (of >= 0) {
+            const uint32_t ahead = __popcll(same & ((1ull << lane) - 1));
+            at = next[of];
+            __builtin_amdgcn_wave_barrier();   // every lane has read before the first one writes
+            if (ahead == 0) next[of] = at + __popcll(same);
+            at += ahead;
+        }
+        __builtin_amdgcn_wave_barrier();
+        return at;
+    };
+    uint32_t earlier[kHeld];
+    if constexpr (kGroups > 0) {
+#pragma unroll
+        for (uint32_t g = 0; g < kGroups; g++) earlier[g] = rank(id[g]);
+    } else {
+        for (uint32_t g = first; g < end; g += 64) rank(g + lane < end ? load_id(a, g + lane, bad) : -1);
     }
     if (bad) set_status(a.status, ZIPCCL_STATUS_BAD_INDEX);
     __syncthreads();
 
     // thread e: the expert's choices in this block, in the blocks before it, and in all
-    uint32_t here = 0, before = 0, all = 0;
+    uint32_t before = 0, all = 0;
     if (tid < E) {
-        for (uint32_t w = 0; w < kSortWaves; w++) here += s_next[w * E + tid];
-        all = here;
         if (a.blocks > 1) {
-            all = 0;
-            for (uint32_t b = 0; b < a.blocks; b++) {
-                const uint32_t c = a.hist[uint64_t(b) * E + tid];
-                all += c;
-                before += b < blockIdx.x ? c : 0;
+            for (uint32_t share = 0; share < kSortThreads / E; share++) {
+                before += s_before[share * E + tid];
+                all += s_all[share * E + tid];
             }
+        } else {
+#pragma unroll
+            for (uint32_t w = 0; w < kSortWaves; w++) all += s_next[w * E + tid];
         }
     }
     // exclusive sum of `all` over the experts
@@ -103,49 +180,45 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const SortArgs
     if (lane == 63) s_wave_sum[wave] = scan;
     __syncthreads();
     uint32_t base = scan - all, total = 0;
+#pragma unroll
     for (uint32_t w = 0; w < kSortWaves; w++) {
         const uint32_t v = s_wave_sum[w];
         base += w < wave ? v : 0;
         total += v;
     }
     if (tid < E) {
-        if (blockIdx.x == 0) a.offsets[tid] = int32_t(base);
-        uint32_t at = base + before;
+        if (block == 0) a.offsets[tid] = int32_t(base);
+        uint32_t at = base + before, count[kSortWaves];
+#pragma unroll
+        for (uint32_t w = 0; w < kSortWaves; w++) count[w] = s_next[w * E + tid];
+#pragma unroll
         for (uint32_t w = 0; w < kSortWaves; w++) {
-            const uint32_t c = s_next[w * E + tid];
             s_next[w * E + tid] = at;
-            at += c;
+            at += count[w];
         }
     }
-    if (blockIdx.x == 0 && tid == 0) a.offsets[E] = int32_t(total);
+    if (block == 0 && tid == 0) a.offsets[E] = int32_t(total);
     // dropped choices leave this many entries at the end of `rows` without a token
-    for (uint32_t s = total + blockIdx.x * kSortThreads + tid; s < a.n; s += a.blocks * kSortThreads) a.rows[s] = -1;
+    for (uint32_t s = total + block * kSortThreads + tid; s < a.n; s += a.blocks * kSortThreads) a.rows[s] = -1;
     __syncthreads();
 
-    // lanes of one expert in a group of 64 are ranked by ballots over the bits of its
-    // number; the first of them moves the wave's counter on
-    const uint32_t bits = E > 1 ? 32 - __builtin_clz(E - 1) : 0;
-    for (uint32_t g = first; g < end; g += 64) {
-        const uint32_t i = g + lane;
-        const int32_t id = i < end ? load_id(a, i, bad) : -1;
-        uint64_t same = __ballot(id >= 0);
-        for (uint32_t b = 0; b < bits; b++) {
-            const bool on = (id >> b) & 1;
-            const uint64_t m = __ballot(on);
-            same &= on ? m : ~m;
-        }
-        if (id >= 0) {
-            const uint32_t rank = __popcll(same & ((1ull << lane) - 1));
-            const uint32_t at = next[id];
-            __builtin_amdgcn_wave_barrier();   // every lane has read before the first one writes
-            if (rank == 0) next[id] = at + __popcll(same);
-            const uint32_t slot = at + rank;
+    const auto place = [&](uint32_t i, int32_t of, uint32_t slot) {
+        if (of >= 0) {
             a.slots[i] = int32_t(slot);
             a.rows[slot] = int32_t(i / a.top_k);
         } else if (i < end) {
             a.slots[i] = -1;
         }
-        __builtin_amdgcn_wave_barrier();
+    };
+    if constexpr (kGroups > 0) {
+#pragma unroll
+        for (uint32_t g = 0; g < kGroups; g++)
+            place(first + 64 * g + lane, id[g], id[g] >= 0 ? next[id[g]] + earlier[g] : 0);
+    } else {
+        for (uint32_t g = first; g < end; g += 64) {
+            const int32_t of = g + lane < end ? load_id(a, g + lane, bad) : -1;
+            place(g + lane, of, rank(of));
+        }
     }
 }
 
@@ -384,9 +457,26 @@ dim3 grid_for(const RowsArgs& a, uint32_t unit, uint32_t chunks_per_lane)
 
 hipError_t launch_moe_sort(const SortArgs& a, hipStream_t s)
 {
-    if (a.blocks > 1) hipLaunchKernelGGL(sort_count_kernel, dim3(a.blocks), dim3(kSortThreads), 0, s, a);
-    hipLaunchKernelGGL(sort_place_kernel, dim3(a.blocks), dim3(kSortThreads), kSortWaves * a.experts * 4, s, a);
-    return hipGetLastError();
+    const dim3 grid(a.blocks > 1 ? (a.blocks + 7) / 8 * 8 : 1), block(kSortThreads);
+    if (a.blocks > 1) hipLaunchKernelGGL(sort_count_kernel, grid, block, 0, s, a);
+    const auto place = [&](void (*kernel)(SortArgs)) -> hipError_t {
+        const uint32_t lds = kSortWaves * a.experts * 4;
+        if (lds > 32768) {   // with the kernel's own arrays more than the 64 KB a launch has by default
+            if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                   hipFuncAttributeMaxDynamicSharedMemorySize, int(lds)))
+                return e;
+        }
+        hipLaunchKernelGGL(kernel, grid, block, lds, s, a);
+        return hipGetLastError();
+    };
+    switch (a.per_block / kSortThreads) {
+        case 1: return place(sort_place_kernel<1>);
+        case 2: return place(sort_place_kernel<2>);
+        case 4: return place(sort_place_kernel<4>);
+        case 8: return place(sort_place_kernel<8>);
+        case 16: return place(sort_place_kernel<16>);
+        default: return place(sort_place_kernel<0>);
+    }
 }
 
 hipError_t launch_moe_dispatch(const RowsArgs& a, hipStream_t s)

@@ -165,7 +165,8 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: building a torch.cuda.Stream takes 3 us, as long as a launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -545,30 +546,35 @@ _DTYPES = {torch.bfloat16: BF16, torch.float32: FP32}
 
 
 def _matrix(t, what, dtype=None):
-    """(address, row stride) of a 2-D row-major tensor."""
-    if t.dim() != 2 or (t.numel() > 0 and t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what} is a 2-D tensor with contiguous rows")
-    if t.dtype not in _DTYPES if dtype is None else t.dtype != dtype:
+    """(address, rows, row length, row stride) of a 2-D row-major tensor."""
+    if t.dim() != 2:
+        raise ValueError(f"{what} is a 2-D tensor")
+    (rows, length), (stride, step) = t.shape, t.stride()
+    if step != 1 and length > 1 and rows > 0:
+        raise ValueError(f"{what} has contiguous rows")
+    if stride < length and rows > 1:
+        raise ValueError(f"{what} has rows that do not overlap")
+    if t.dtype not in _DTYPES if dtype is None else t.dtype is not dtype:
         raise ValueError(f"{what} is {t.dtype}")
-    return t.data_ptr(), max(t.stride(0), t.shape[1])
+    return t.data_ptr(), rows, length, stride if stride > length else length
 
 
 def _vector(t, n, dtype, what):
     """Address of a contiguous tensor of at least n values."""
-    if t.dtype != dtype or t.numel() < n or not t.is_contiguous():
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{what} is a contiguous {dtype} tensor of at least {n} values")
     return t.data_ptr()
 
 
-def _slots(slots, tokens, what="slots"):
+def _slots(slots, tokens):
     if slots.dim() != 2 or slots.shape[0] != tokens:
-        raise ValueError(f"{what} is tokens x top_k, {tokens} tokens")
-    return _vector(slots, 0, torch.int32, what), slots.shape[1]
+        raise ValueError(f"slots is tokens x top_k, {tokens} tokens")
+    return _vector(slots, 0, torch.int32, "slots"), slots.shape[1]
 
 
-def _same_rows(a, b, what):
-    if a.shape[1] != b.shape[1] or a.dtype != b.dtype:
-        raise ValueError(f"{what} have the same row length and dtype")
+def _same(a, b, what):
+    if a != b:
+        raise ValueError(f"{what} agree: {a} and {b}")
 
 
 def moe_sort(experts, num_experts: int, offsets, rows, slots, workspace, status=None, stream=None):
@@ -576,12 +582,10 @@ def moe_sort(experts, num_experts: int, offsets, rows, slots, workspace, status=
     top-k indices; negative: dropped).  Writes offsets (int32, num_experts + 1), rows
     (int32, tokens * top_k) and slots (int32, tokens x top_k).  workspace:
     MOE_SORT_WORKSPACE_BYTES device bytes."""
-    if experts.dim() != 2 or experts.dtype not in (torch.int32, torch.int64) or \
-            (experts.numel() > 0 and experts.shape[1] > 1 and experts.stride(1) != 1):
-        raise ValueError("experts is a 2-D int32 or int64 tensor with contiguous rows")
-    T, K = experts.shape
-    _check(_lib.zipccl_moe_sort(experts.data_ptr(), experts.element_size(), max(experts.stride(0), K), T, K,
-                                num_experts, _vector(offsets, num_experts + 1, torch.int32, "offsets"),
+    wide = experts.dtype is torch.int64
+    ep, T, K, stride = _matrix(experts, "experts", torch.int64 if wide else torch.int32)
+    _check(_lib.zipccl_moe_sort(ep, 8 if wide else 4, stride, T, K, num_experts,
+                                _vector(offsets, num_experts + 1, torch.int32, "offsets"),
                                 _vector(rows, T * K, torch.int32, "rows"),
                                 _vector(slots, T * K, torch.int32, "slots"), workspace.data_ptr(),
                                 _nbytes(workspace), _ptr(status), _stream(stream)), "zipccl_moe_sort")
@@ -589,52 +593,47 @@ def moe_sort(experts, num_experts: int, offsets, rows, slots, workspace, status=
 
 def moe_dispatch(x, slots, y, status=None, stream=None):
     """zipccl_moe_dispatch: y[slots[t, k]] = x[t]."""
-    xp, xs = _matrix(x, "x")
-    yp, ys = _matrix(y, "y")
-    _same_rows(x, y, "x and y")
-    sp, K = _slots(slots, x.shape[0])
-    _check(_lib.zipccl_moe_dispatch(xp, xs, sp, x.shape[0], K, x.shape[1], _DTYPES[x.dtype], yp, y.shape[0], ys,
-                                    _ptr(status), _stream(stream)), "zipccl_moe_dispatch")
+    xp, T, H, xs = _matrix(x, "x")
+    yp, M, yh, ys = _matrix(y, "y", x.dtype)
+    _same(H, yh, "the rows of x and y")
+    sp, K = _slots(slots, T)
+    _check(_lib.zipccl_moe_dispatch(xp, xs, sp, T, K, H, _DTYPES[x.dtype], yp, M, ys, _ptr(status),
+                                    _stream(stream)), "zipccl_moe_dispatch")
 
 
 def moe_dispatch_backward(dy, slots, dx, status=None, stream=None):
     """zipccl_moe_dispatch_backward: dx[t] = sum over k of dy[slots[t, k]]."""
-    yp, ys = _matrix(dy, "dy")
-    xp, xs = _matrix(dx, "dx")
-    _same_rows(dy, dx, "dy and dx")
-    sp, K = _slots(slots, dx.shape[0])
-    _check(_lib.zipccl_moe_dispatch_backward(yp, dy.shape[0], ys, sp, dx.shape[0], K, dx.shape[1],
-                                             _DTYPES[dy.dtype], xp, xs, _ptr(status), _stream(stream)),
-           "zipccl_moe_dispatch_backward")
+    yp, M, H, ys = _matrix(dy, "dy")
+    xp, T, xh, xs = _matrix(dx, "dx", dy.dtype)
+    _same(H, xh, "the rows of dy and dx")
+    sp, K = _slots(slots, T)
+    _check(_lib.zipccl_moe_dispatch_backward(yp, M, ys, sp, T, K, H, _DTYPES[dy.dtype], xp, xs, _ptr(status),
+                                             _stream(stream)), "zipccl_moe_dispatch_backward")
 
 
 def moe_combine(y, slots, weights, out, status=None, stream=None):
     """zipccl_moe_combine: out[t] = sum over k of weights[t, k] * y[slots[t, k]] (weights
     float32, or None for 1)."""
-    yp, ys = _matrix(y, "y")
-    op, os_ = _matrix(out, "out")
-    _same_rows(y, out, "y and out")
-    sp, K = _slots(slots, out.shape[0])
-    wp = None if weights is None else _vector(weights, out.shape[0] * K, torch.float32, "weights")
-    _check(_lib.zipccl_moe_combine(yp, y.shape[0], ys, sp, wp, out.shape[0], K, out.shape[1], _DTYPES[y.dtype], op,
-                                   os_, _ptr(status), _stream(stream)), "zipccl_moe_combine")
+    yp, M, H, ys = _matrix(y, "y")
+    op, T, oh, os_ = _matrix(out, "out", y.dtype)
+    _same(H, oh, "the rows of y and out")
+    sp, K = _slots(slots, T)
+    wp = None if weights is None else _vector(weights, T * K, torch.float32, "weights")
+    _check(_lib.zipccl_moe_combine(yp, M, ys, sp, wp, T, K, H, _DTYPES[y.dtype], op, os_, _ptr(status),
+                                   _stream(stream)), "zipccl_moe_combine")
 
 
 def moe_combine_backward(dout, y, slots, weights, dy, dweights, status=None, stream=None):
     """zipccl_moe_combine_backward: dy[slots[t, k]] = weights[t, k] * dout[t] and
     dweights[t, k] = <dout[t], y[slots[t, k]]>."""
-    gp, gs = _matrix(dout, "dout")
-    yp, ys = _matrix(y, "y")
-    dp, ds = _matrix(dy, "dy")
-    _same_rows(dout, y, "dout and y")
-    _same_rows(y, dy, "y and dy")
-    if y.shape[0] != dy.shape[0]:
-        raise ValueError("y and dy have the same rows")
-    T = dout.shape[0]
+    gp, T, gh, gs = _matrix(dout, "dout")
+    yp, M, H, ys = _matrix(y, "y", dout.dtype)
+    dp, dm, dh, ds = _matrix(dy, "dy", dout.dtype)
+    _same(H, gh, "the rows of y and dout")
+    _same((M, H), (dm, dh), "y and dy")
     sp, K = _slots(slots, T)
-    _check(_lib.zipccl_moe_combine_backward(gp, gs, yp, y.shape[0], ys, sp,
-                                            _vector(weights, T * K, torch.float32, "weights"), T, K, y.shape[1],
-                                            _DTYPES[y.dtype], dp, ds,
+    _check(_lib.zipccl_moe_combine_backward(gp, gs, yp, M, ys, sp, _vector(weights, T * K, torch.float32, "weights"),
+                                            T, K, H, _DTYPES[y.dtype], dp, ds,
                                             _vector(dweights, T * K, torch.float32, "dweights"), _ptr(status),
                                             _stream(stream)), "zipccl_moe_combine_backward")
 
@@ -643,14 +642,13 @@ def quantize_rows(x, q, scales, slots=None, status=None, stream=None):
     """zipccl_quantize_rows: BF16 rows x to int8 rows q (row stride a multiple of ROW_PAD,
     at least as long as x's rows) with float32 scales, to every slot of a token or, without
     slots, row by row."""
-    xp, xs = _matrix(x, "x", torch.bfloat16)
-    qp, qs = _matrix(q, "q", torch.int8)
-    if q.shape[1] < x.shape[1]:
+    xp, T, H, xs = _matrix(x, "x", torch.bfloat16)
+    qp, M, wide, qs = _matrix(q, "q", torch.int8)
+    if wide < H:
         raise ValueError("q's rows hold x's rows")
-    sp, K = (None, 1) if slots is None else _slots(slots, x.shape[0])
-    _check(_lib.zipccl_quantize_rows(xp, xs, x.shape[0], x.shape[1], sp, K, qp, q.shape[0], qs,
-                                     _vector(scales, q.shape[0], torch.float32, "scales"), _ptr(status),
-                                     _stream(stream)), "zipccl_quantize_rows")
+    sp, K = (None, 1) if slots is None else _slots(slots, T)
+    _check(_lib.zipccl_quantize_rows(xp, xs, T, H, sp, K, qp, M, qs, _vector(scales, M, torch.float32, "scales"),
+                                     _ptr(status), _stream(stream)), "zipccl_quantize_rows")
 
 
 def experts_product(q, scales, w, w_scales, row_len: int, out, offsets=None, status=None, stream=None):
@@ -658,20 +656,20 @@ def experts_product(q, scales, w, w_scales, row_len: int, out, offsets=None, sta
     experts x outputs x stride (or outputs x stride for one), w_scales float32, experts x
     outputs; row_len: values of a row without its padding; out: rows x outputs, bfloat16
     or float32; offsets: int32, experts + 1 (None: one expert)."""
-    qp, qs = _matrix(q, "q", torch.int8)
-    op, os_ = _matrix(out, "out")
-    if w.dim() not in (2, 3) or w.dtype != torch.int8 or not w.is_contiguous():
-        raise ValueError("w is a contiguous int8 tensor, experts x outputs x row stride")
-    E, N = (1 if w.dim() == 2 else w.shape[0]), w.shape[-2]
-    if out.shape[0] != q.shape[0] or out.shape[1] != N:
-        raise ValueError("out is q's rows x w's outputs")
-    if row_len > q.shape[1] or row_len > w.shape[-1]:
+    qp, M, wide, qs = _matrix(q, "q", torch.int8)
+    op, om, on, os_ = _matrix(out, "out")
+    if w.dim() not in (2, 3):
+        raise ValueError("w is experts x outputs x row stride")
+    E, N, ws = w.shape if w.dim() == 3 else (1, *w.shape)
+    _same((om, on), (M, N), "out, and q's rows x w's outputs")
+    if row_len > wide or row_len > ws:
         raise ValueError("row_len is at most the row length of q and w")
-    _check(_lib.zipccl_experts_product(qp, qs, _vector(scales, q.shape[0], torch.float32, "scales"), q.shape[0],
-                                       w.data_ptr(), w.shape[-1], _vector(w_scales, E * N, torch.float32, "w_scales"),
-                                       E, N, row_len, None if offsets is None else
-                                       _vector(offsets, E + 1, torch.int32, "offsets"), op, os_, _DTYPES[out.dtype],
-                                       _ptr(status), _stream(stream)), "zipccl_experts_product")
+    _check(_lib.zipccl_experts_product(qp, qs, _vector(scales, M, torch.float32, "scales"), M,
+                                       _vector(w, 0, torch.int8, "w"), ws,
+                                       _vector(w_scales, E * N, torch.float32, "w_scales"), E, N, row_len,
+                                       None if offsets is None else _vector(offsets, E + 1, torch.int32, "offsets"),
+                                       op, os_, _DTYPES[out.dtype], _ptr(status), _stream(stream)),
+           "zipccl_experts_product")
 
 
 # ------------------------------------------------------------------------------------

@@ -126,6 +126,8 @@ def test_binding_checks_shapes_and_types(Z):
             lambda: Z.moe_dispatch(bf, i32.long(), bf),                            # slots are int32
             lambda: Z.moe_dispatch(bf, i32[:3], bf),                               # slots of other tokens
             lambda: Z.moe_dispatch(bf.t(), i32, bf),                               # columns are not rows
+            lambda: Z.moe_dispatch(bf[:1].expand(4, 10), i32, bf),                 # one row four times
+            lambda: Z.moe_dispatch(bf[0], i32, bf),
             lambda: Z.moe_combine(f32, i32, one[:7], f32[:4]),                     # too few weights
             lambda: Z.moe_combine(f32, i32, one.double(), f32[:4]),
             lambda: Z.moe_combine_backward(f32[:4], f32, i32, one, f32[:7], one),  # dy of other rows
