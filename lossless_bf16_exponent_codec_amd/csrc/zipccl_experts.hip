@@ -29,10 +29,16 @@ __device__ inline void set_status(uint32_t* status, uint32_t bits)
     if (status) atomicOr(status, bits);
 }
 
-__device__ inline uint32_t bf16_rne(float f)
+// Two values rounded to BF16 (to nearest even), NaN as 0x7FC0.
+__device__ inline uint32_t bf16_pair(float lo, float hi)
 {
-    const uint32_t u = __float_as_uint(f);
-    return f != f ? 0x7FC0u : (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    const f2 v = {lo == lo ? lo : __uint_as_float(0x7FC00000u), hi == hi ? hi : __uint_as_float(0x7FC00000u)};
+    const b2 b = __builtin_convertvector(v, b2);
+    uint32_t r;
+    __builtin_memcpy(&r, &b, 4);
+    return r;
 }
 
 // ------------------------------------------------------------------------------------
@@ -206,9 +212,9 @@ struct Outputs {
     __device__ inline Outputs(const ProductArgs& a, uint32_t expert, uint32_t first)
         : n(first), count(first < a.outputs ? min(8u, a.outputs - first) : 0u)
     {
-        const float* from = a.w_scales + uint64_t(expert) * a.outputs + n;
+        const float* from = a.w_scales + uint64_t(expert) * a.outputs;
 #pragma unroll
-        for (uint32_t r = 0; r < 8; r++) ws[r] = r < count ? from[r] : 0.0f;
+        for (uint32_t r = 0; r < 8; r++) ws[r] = from[min(n + r, a.outputs - 1)];   // no use of a value, so no wait, here
     }
 
     // v: sum * row scale
@@ -231,7 +237,7 @@ struct Outputs {
             uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + at;
             uint32_t b[4];
 #pragma unroll
-            for (uint32_t r = 0; r < 4; r++) b[r] = bf16_rne(f[2 * r]) | bf16_rne(f[2 * r + 1]) << 16;
+            for (uint32_t r = 0; r < 4; r++) b[r] = bf16_pair(f[2 * r], f[2 * r + 1]);
             if (count == 8) {
                 __builtin_memcpy(o, b, 16);
             } else {
@@ -301,6 +307,7 @@ __device__ inline void product_tile(const ProductArgs& a, uint8_t* s_ring, uint3
     constexpr uint32_t kRows = 64 * kM, kSlot = slot_bytes(kM, kN);
     constexpr uint32_t kLoads = 2 * (kM + kN), kEarly = kLoads / 2;   // loads of a thread per slab
     constexpr uint32_t kProducts = kM * kN;                           // products of a quarter slab
+    constexpr uint32_t kPerRow = 4 * kN;                              // lanes that store a row of a wave
     const uint32_t lane = lane_id();
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int8_t* q = a.q + uint64_t(row0) * a.q_stride;
@@ -348,6 +355,12 @@ __device__ inline void product_tile(const ProductArgs& a, uint8_t* s_ring, uint3
     };
 #pragma unroll
     for (uint32_t s = 0; s < kSlots; s++) load(s, 0, kLoads);
+    // the scales this lane needs at the end, requested now
+    float scale[kM];
+#pragma unroll
+    for (uint32_t i = 0; i < kM; i++) scale[i] = a.scales[row0 + min(wm + 32 * i + (lane & 31), rows - 1)];
+    const uint32_t n = n0 + wn + 8 * (lane % kPerRow);   // the 8 outputs it stores of each row
+    const Outputs to(a, expert, n);
     wait_loads_and_meet<(kSlots - 1) * kLoads>();
     read(0, 0);
     for (uint32_t s = 0; s < a.slabs; s++) {
@@ -374,13 +387,7 @@ __device__ inline void product_tile(const ProductArgs& a, uint8_t* s_ring, uint3
     // Strips of 32 rows change hands in the wave's own part of LDS so that a lane gets 8
     // outputs in a row and a store covers whole rows of the wave's outputs.
     constexpr uint32_t kPitch = 32 * kN * 4 + 16;       // bytes; the 16 spread rows over the banks
-    constexpr uint32_t kPerRow = 4 * kN;                // lanes of a row
     static_assert(4 * 32 * kPitch <= kSlots * kSlot, "strips fit the ring");
-    float scale[kM];
-#pragma unroll
-    for (uint32_t i = 0; i < kM; i++) scale[i] = a.scales[row0 + min(wm + 32 * i + (lane & 31), rows - 1)];
-    const uint32_t n = n0 + wn + 8 * (lane % kPerRow);
-    const Outputs to(a, expert, n);
     wait_loads_and_meet<0>();   // the surplus loads have landed and every wave is done reading: the ring is free
     uint8_t* strip = s_ring + wave * (32 * kPitch);
 #pragma unroll
@@ -395,7 +402,7 @@ __device__ inline void product_tile(const ProductArgs& a, uint8_t* s_ring, uint3
                 *reinterpret_cast<v4f*>(strip + (lane & 31) * kPitch + (32 * j + 8 * g + 4 * half) * 4) = v;
             }
         __builtin_amdgcn_wave_barrier();
-#pragma unroll 2
+#pragma unroll 4
         for (uint32_t at = lane / kPerRow; at < 32; at += 64 / kPerRow) {
             const uint32_t row = wm + 32 * i + at;
             if (row >= rows) break;
@@ -535,8 +542,8 @@ hipError_t launch_experts_product(const ProductArgs& a, hipStream_t s)
     if (v && *v == 'e') return launch_tiles<1, 1, 2, 4>(a, s);
     if (v && *v == 'f') return launch_tiles<1, 1, 4, 2>(a, s);
     if (v && *v == 'g') return launch_large(a, s);
-    if (v && *v == 'h') return launch_tiles<4, 2, 2, 1>(a, s);
-    if (v && *v == 'i') return launch_tiles<2, 4, 2, 1>(a, s);
+    if (v && *v == 'h') return launch_tiles<1, 1, 8, 1>(a, s);
+    if (v && *v == 'i') return launch_tiles<1, 1, 5, 2>(a, s);
     return use_large(a) ? launch_large(a, s) : launch_tiles<2, 2, 2, 2>(a, s);
 }
 
