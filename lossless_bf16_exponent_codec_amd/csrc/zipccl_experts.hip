@@ -10,7 +10,6 @@
 // which tiles and waves add them does not show.
 #include <hip/hip_runtime.h>
 
-#include <cstdlib>
 #include "zipccl.h"
 #include "zipccl_moe_internal.h"
 
@@ -257,6 +256,13 @@ __device__ inline void wait_loads_and_meet()
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// The same for one wave alone.
+template <uint32_t N>
+__device__ inline void wait_loads()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
 // All waves: no LDS read is in flight.
 __device__ inline void wait_reads_and_meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
@@ -473,6 +479,107 @@ __global__ __launch_bounds__(kTileThreads, 1) void product_large_kernel(const Pr
     if (r < rows && n0 < a.outputs) product_tile<2, 2, 2>(a, s_ring, expert, row0 + r, min(rows - r, 128u), n0);
 }
 
+// A tile of up to 64 rows x 32 outputs per workgroup, the row length split over its 4
+// waves: for calls whose tiles do not fill the GPU, where the time is that of one tile's
+// chain of steps.  Each wave has a ring of its own and meets no other until the end, when
+// the 4 partial sums (whole numbers: in any order) are joined through LDS.
+constexpr uint32_t kSplitOuts = 32, kSplitSlots = 3;
+constexpr uint32_t kSplitSlot = (64 + kSplitOuts) * kSlab, kSplitWaves = kTileThreads / 64;
+constexpr uint32_t kSplitLds = kSplitWaves * kSplitSlots * kSplitSlot;
+
+__global__ __launch_bounds__(kTileThreads, 1) void product_split_kernel(const ProductArgs a)
+{
+    constexpr uint32_t kLoads = kSplitSlot / 1024, kPitch = kSplitOuts + 4;   // pitch: values of a row of sums
+    extern __shared__ __attribute__((aligned(1024))) uint8_t s_ring[];
+    const uint32_t across = (a.outputs + kSplitOuts - 1) / kSplitOuts;
+    uint32_t expert, row0, rows;
+    RowTiles<64> map(a);
+    if (!map.find(a, blockIdx.x / across, expert, row0, rows)) return;
+    const uint32_t n0 = blockIdx.x % across * kSplitOuts;
+    const uint32_t tid = threadIdx.x, lane = lane_id();
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int8_t* q = a.q + uint64_t(row0) * a.q_stride;
+    const int8_t* w = a.w + (uint64_t(expert) * a.outputs + n0) * a.w_stride;
+    uint8_t* ring = s_ring + wave * kSplitSlots * kSplitSlot;
+
+    // what the end needs, requested now: thread t stores outputs 8 (t % 4) .. of row t / 4
+    const uint32_t out_row = tid / 4;
+    const float scale = a.scales[row0 + min(out_row, rows - 1)];
+    const Outputs to(a, expert, n0 + 8 * (tid & 3));
+
+    // the same arrangement of rows and pieces as in product_tile
+    uint32_t from[kLoads];
+#pragma unroll
+    for (uint32_t i = 0; i < kLoads; i++) {
+        const uint32_t r = 8 * i + lane / 8, piece = (lane & 7) ^ ((r >> 1) & 7);
+        from[i] = (i < 8 ? min(r, rows - 1) * uint32_t(a.q_stride)
+                         : min(r - 64, a.outputs - 1 - n0) * uint32_t(a.w_stride)) + 16 * piece;
+    }
+    const uint32_t per = (a.slabs + kSplitWaves - 1) / kSplitWaves;
+    const uint32_t first = min(wave * per, a.slabs), end = min(first + per, a.slabs);
+    const auto load = [&](uint32_t s) {
+        const uint32_t at = min(s, a.slabs - 1) * kSlab;
+        uint8_t* slot = ring + (s - first) % kSplitSlots * kSplitSlot;
+#pragma unroll
+        for (uint32_t i = 0; i < kLoads; i++) load_lds((i < 8 ? q : w) + at + from[i], slot + 1024 * i);
+    };
+    v16i acc[2] = {};
+    v4i fq[2][4][2], fw[2][4];
+    const uint32_t half = lane >> 5, turn = (lane >> 1) & 7;
+    const auto read = [&](uint32_t to, uint32_t s) {
+        const uint8_t* slot = ring + (s - first) % kSplitSlots * kSplitSlot + (lane & 31) * kSlab;
+#pragma unroll
+        for (uint32_t k = 0; k < 4; k++) {
+            const uint32_t at = ((2 * k + half) ^ turn) * 16;
+            fq[to][k][0] = *reinterpret_cast<const v4i*>(slot + at);
+            fq[to][k][1] = *reinterpret_cast<const v4i*>(slot + at + 32 * kSlab);
+            fw[to][k] = *reinterpret_cast<const v4i*>(slot + at + 64 * kSlab);
+        }
+    };
+    if (first < end) {
+#pragma unroll
+        for (uint32_t s = 0; s < kSplitSlots; s++) load(first + s);
+        wait_loads<(kSplitSlots - 1) * kLoads>();
+        read(0, first);
+        for (uint32_t s0 = first; s0 < end; s0 += 2) {
+#pragma unroll
+            for (uint32_t u = 0; u < 2; u++) {
+                const uint32_t s = s0 + u;   // a surplus odd step reads a surplus slab and is not added
+                wait_loads<(kSplitSlots - 2) * kLoads>();   // slab s is in registers, slab s + 1 has landed
+                read(u ^ 1, s + 1);
+                load(s + kSplitSlots);
+                if (s < end) {
+#pragma unroll
+                    for (uint32_t k = 0; k < 4; k++) {
+                        acc[0] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[u][k], fq[u][k][0], acc[0], 0, 0, 0);
+                        acc[1] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[u][k], fq[u][k][1], acc[1], 0, 0, 0);
+                    }
+                }
+            }
+        }
+    }
+    wait_loads_and_meet<0>();
+    int32_t* sums = reinterpret_cast<int32_t*>(s_ring);   // [wave][row][kPitch]
+#pragma unroll
+    for (uint32_t i = 0; i < 2; i++)
+#pragma unroll
+        for (uint32_t g = 0; g < 4; g++) {
+            const v4i v = {acc[i][4 * g], acc[i][4 * g + 1], acc[i][4 * g + 2], acc[i][4 * g + 3]};
+            *reinterpret_cast<v4i*>(sums + (wave * 64 + 32 * i + (lane & 31)) * kPitch + 8 * g + 4 * half) = v;
+        }
+    __syncthreads();
+    if (out_row < rows) {
+        v4i lo = {}, hi = {};
+#pragma unroll
+        for (uint32_t v = 0; v < kSplitWaves; v++) {
+            const v4i* at = reinterpret_cast<const v4i*>(sums + (v * 64 + out_row) * kPitch + 8 * (tid & 3));
+            lo += at[0];
+            hi += at[1];
+        }
+        to.store(a, row0 + out_row, __builtin_convertvector(lo, v4f) * scale, __builtin_convertvector(hi, v4f) * scale);
+    }
+}
+
 // Row tiles that any split of `rows` rows over the experts can need.
 uint64_t most_tiles(const ProductArgs& a, uint32_t per_tile)
 {
@@ -491,9 +598,19 @@ hipError_t launch_quantize_rows(const QuantArgs& a, hipStream_t s)
 
 namespace {
 
-uint64_t tile_workgroups(const ProductArgs& a, uint32_t m, uint32_t n)
+// Allows a kernel the LDS its launch asks for (past the 64 KB a launch has by default).
+hipError_t allow_lds(const void* kernel, uint32_t bytes)
 {
-    return (most_tiles(a, 64 * m) * ((a.outputs + 64 * n - 1) / (64 * n)) + kXcds - 1) / kXcds * kXcds;
+    return bytes > 65536 ? hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, int(bytes))
+                         : hipSuccess;
+}
+
+uint64_t columns(const ProductArgs& a, uint32_t outs) { return (a.outputs + outs - 1) / outs; }
+
+template <uint32_t kM, uint32_t kN>
+uint64_t tile_workgroups(const ProductArgs& a)
+{
+    return (most_tiles(a, 64 * kM) * columns(a, 64 * kN) + kXcds - 1) / kXcds * kXcds;
 }
 
 template <uint32_t kM, uint32_t kN, uint32_t kSlots, uint32_t kPerCu>
@@ -501,50 +618,70 @@ hipError_t launch_tiles(const ProductArgs& a, hipStream_t s)
 {
     constexpr uint32_t lds = tile_lds(kM, kN, kSlots);
     const auto kernel = product_tile_kernel<kM, kN, kSlots, kPerCu>;
-    if (lds > 65536) {
-        if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                               hipFuncAttributeMaxDynamicSharedMemorySize, int(lds)))
-            return e;
-    }
-    hipLaunchKernelGGL(kernel, dim3(uint32_t(tile_workgroups(a, kM, kN))), dim3(kTileThreads), lds, s, a);
+    if (hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), lds)) return e;
+    hipLaunchKernelGGL(kernel, dim3(uint32_t(tile_workgroups<kM, kN>(a))), dim3(kTileThreads), lds, s, a);
     return hipGetLastError();
 }
 
 // most_tiles bounds the whole tiles; cutting the last ones adds 3 workgroups for each
-uint64_t large_workgroups(const ProductArgs& a) { return tile_workgroups(a, 4, 4) + 3 * kCutTiles; }
+uint64_t large_workgroups(const ProductArgs& a) { return tile_workgroups<4, 4>(a) + 3 * kCutTiles; }
 
-hipError_t launch_large(const ProductArgs& a, hipStream_t s)
+uint64_t split_workgroups(const ProductArgs& a) { return most_tiles(a, 64) * columns(a, kSplitOuts); }
+
+// Which kernel, by the tiles that rows spread evenly over the experts would make (the
+// host does not know the offsets).  Times in us, weights outputs x row_len:
+//  - one round of split workgroups or less: split (1 expert, 64 rows, 2048 x 7168: 9.2
+//    against 18.1 for 64 x 64 tiles; 4 experts: 15.2 and 19.3; 8 experts, two rounds: 29.9
+//    and 22.1);
+//  - up to 64 rows for an expert: 64 x 64, where the weights' reads are what counts (8
+//    experts, 8192 x 4096: 39 at 64 x 64, 41 at 128 x 128), four slabs deep while a CU has
+//    no second workgroup to run meanwhile (8 experts, 2048 x 7168: 20 and 26 at two);
+//  - 256 x 256 from 192 rows on when there is a round of it (8 experts, 2048 rows each,
+//    2048 x 7168: 212 against 246 at 128 x 128; 512 rows each, half a round: 78 and 62);
+//  - else 128 x 128 (64 x 64 at 128 rows, 32 experts, 2048 x 7168: 148 and 105).
+enum class Shape { split, narrow_deep, narrow, square, large };
+
+Shape choose(const ProductArgs& a)
 {
-    constexpr uint32_t lds = tile_lds(4, 4, 2);
-    if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(product_large_kernel),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, int(lds)))
-        return e;
-    hipLaunchKernelGGL(product_large_kernel, dim3(uint32_t(large_workgroups(a))), dim3(kTileThreads), lds, s, a);
-    return hipGetLastError();
+    const uint64_t parts = a.experts < a.rows ? a.experts : a.rows, each = (a.rows + parts - 1) / parts;
+    const auto tiles = [&](uint32_t rows, uint32_t outs) { return parts * ((each + rows - 1) / rows) * columns(a, outs); };
+    if (tiles(64, kSplitOuts) <= kCus) return Shape::split;
+    if (each <= 64) return tiles(64, 64) <= kCus + kCus / 2 ? Shape::narrow_deep : Shape::narrow;
+    return each >= 192 && tiles(256, 256) >= kCus ? Shape::large : Shape::square;
 }
-
-bool use_large(const ProductArgs& a) { return tile_workgroups(a, 4, 4) >= 256; }
 
 }  // namespace
 
 uint64_t product_workgroups(const ProductArgs& a)
 {
-    return use_large(a) ? large_workgroups(a) : tile_workgroups(a, 2, 2);
+    switch (choose(a)) {
+        case Shape::split: return split_workgroups(a);
+        case Shape::large: return large_workgroups(a);
+        case Shape::square: return tile_workgroups<2, 2>(a);
+        default: return tile_workgroups<1, 1>(a);
+    }
 }
 
 hipError_t launch_experts_product(const ProductArgs& a, hipStream_t s)
 {
-    const char* v = getenv("ZV");
-    if (v && *v == 'a') return launch_tiles<1, 2, 2, 3>(a, s);
-    if (v && *v == 'b') return launch_tiles<1, 2, 4, 1>(a, s);
-    if (v && *v == 'c') return launch_tiles<2, 2, 2, 2>(a, s);
-    if (v && *v == 'd') return launch_tiles<2, 2, 4, 1>(a, s);
-    if (v && *v == 'e') return launch_tiles<1, 1, 2, 4>(a, s);
-    if (v && *v == 'f') return launch_tiles<1, 1, 4, 2>(a, s);
-    if (v && *v == 'g') return launch_large(a, s);
-    if (v && *v == 'h') return launch_tiles<1, 1, 8, 1>(a, s);
-    if (v && *v == 'i') return launch_tiles<1, 1, 5, 2>(a, s);
-    return use_large(a) ? launch_large(a, s) : launch_tiles<2, 2, 2, 2>(a, s);
+    switch (choose(a)) {
+        case Shape::narrow_deep: return launch_tiles<1, 1, 4, 2>(a, s);
+        case Shape::narrow: return launch_tiles<1, 1, 2, 4>(a, s);
+        case Shape::square: return launch_tiles<2, 2, 2, 2>(a, s);
+        case Shape::split: {
+            if (hipError_t e = allow_lds(reinterpret_cast<const void*>(product_split_kernel), kSplitLds)) return e;
+            hipLaunchKernelGGL(product_split_kernel, dim3(uint32_t(split_workgroups(a))), dim3(kTileThreads), kSplitLds,
+                               s, a);
+            break;
+        }
+        case Shape::large: {
+            constexpr uint32_t lds = tile_lds(4, 4, 2);
+            if (hipError_t e = allow_lds(reinterpret_cast<const void*>(product_large_kernel), lds)) return e;
+            hipLaunchKernelGGL(product_large_kernel, dim3(uint32_t(large_workgroups(a))), dim3(kTileThreads), lds, s, a);
+            break;
+        }
+    }
+    return hipGetLastError();
 }
 
 }  // namespace zc
