@@ -633,20 +633,25 @@ uint64_t split_workgroups(const ProductArgs& a) { return most_tiles(a, 64) * col
 //  - one round of split workgroups or less: split (1 expert, 64 rows, 2048 x 7168: 9.2
 //    against 18.1 for 64 x 64 tiles; 4 experts: 15.2 and 19.3; 8 experts, two rounds: 29.9
 //    and 22.1);
-//  - up to 64 rows for an expert: 64 x 64, where the weights' reads are what counts (8
-//    experts, 8192 x 4096: 39 at 64 x 64, 41 at 128 x 128), four slabs deep while a CU has
-//    no second workgroup to run meanwhile (8 experts, 2048 x 7168: 20 and 26 at two);
+//  - up to 64 rows for an expert the weights' reads are what counts.  Few tiles of 64 x 64:
+//    four slabs deep while a CU has no second workgroup to run meanwhile (8 experts, 2048 x
+//    7168: 20 and 26 at two), else two slabs and four workgroups (16 experts: 35 and 35).
+//    Many: 64 x 128, which read the rows half as often (256 choices over 32 skewed
+//    experts, 2048 x 7168: 78 against 94 at 64 x 64; 1024 over 128: 279 and 286);
 //  - 256 x 256 from 192 rows on when there is a round of it (8 experts, 2048 rows each,
 //    2048 x 7168: 212 against 246 at 128 x 128; 512 rows each, half a round: 78 and 62);
 //  - else 128 x 128 (64 x 64 at 128 rows, 32 experts, 2048 x 7168: 148 and 105).
-enum class Shape { split, narrow_deep, narrow, square, large };
+enum class Shape { split, narrow_deep, narrow, wide, square, large };
 
 Shape choose(const ProductArgs& a)
 {
     const uint64_t parts = a.experts < a.rows ? a.experts : a.rows, each = (a.rows + parts - 1) / parts;
     const auto tiles = [&](uint32_t rows, uint32_t outs) { return parts * ((each + rows - 1) / rows) * columns(a, outs); };
     if (tiles(64, kSplitOuts) <= kCus) return Shape::split;
-    if (each <= 64) return tiles(64, 64) <= kCus + kCus / 2 ? Shape::narrow_deep : Shape::narrow;
+    if (each <= 64) {
+        const uint64_t n = tiles(64, 64);
+        return n <= kCus + kCus / 2 ? Shape::narrow_deep : n <= 3 * kCus ? Shape::narrow : Shape::wide;
+    }
     return each >= 192 && tiles(256, 256) >= kCus ? Shape::large : Shape::square;
 }
 
@@ -658,6 +663,7 @@ uint64_t product_workgroups(const ProductArgs& a)
         case Shape::split: return split_workgroups(a);
         case Shape::large: return large_workgroups(a);
         case Shape::square: return tile_workgroups<2, 2>(a);
+        case Shape::wide: return tile_workgroups<1, 2>(a);
         default: return tile_workgroups<1, 1>(a);
     }
 }
@@ -667,6 +673,7 @@ hipError_t launch_experts_product(const ProductArgs& a, hipStream_t s)
     switch (choose(a)) {
         case Shape::narrow_deep: return launch_tiles<1, 1, 4, 2>(a, s);
         case Shape::narrow: return launch_tiles<1, 1, 2, 4>(a, s);
+        case Shape::wide: return launch_tiles<1, 2, 2, 3>(a, s);
         case Shape::square: return launch_tiles<2, 2, 2, 2>(a, s);
         case Shape::split: {
             if (hipError_t e = allow_lds(reinterpret_cast<const void*>(product_split_kernel), kSplitLds)) return e;
