@@ -236,18 +236,39 @@ template <> struct Raw<16> { typedef uint4 type; };
 template <> struct Raw<4> { typedef uint32_t type; };
 template <> struct Raw<2> { typedef uint16_t type; };
 
+// The rows by expert, 8 times the tokens' bytes at 8 choices, are read and written with
+// non-temporal accesses; the tokens' rows, which fit the Infinity Cache where those do not,
+// with plain ones (16384 tokens of 7168 to 8 rows each: dispatch 346 us, 385 with plain
+// stores, 425 with non-temporal loads; combine 345 us, 400 with plain loads).
+typedef uint32_t Quad __attribute__((ext_vector_type(4), aligned(2)));
+
 template <uint32_t BYTES>
 __device__ inline typename Raw<BYTES>::type load_raw(const uint8_t* p)
 {
-    typename Raw<BYTES>::type v;
-    __builtin_memcpy(&v, BYTES > 2 ? __builtin_assume_aligned(p, 2) : p, BYTES);
-    return v;
+    if constexpr (BYTES == 16) {
+        const Quad v = __builtin_nontemporal_load(reinterpret_cast<const Quad*>(p));
+        return make_uint4(v.x, v.y, v.z, v.w);
+    } else {
+        return *reinterpret_cast<const typename Raw<BYTES>::type*>(p);
+    }
+}
+
+template <uint32_t BYTES>
+__device__ inline typename Raw<BYTES>::type load_kept(const uint8_t* p)
+{
+    if constexpr (BYTES == 16) {
+        const Quad v = *reinterpret_cast<const Quad*>(p);
+        return make_uint4(v.x, v.y, v.z, v.w);
+    } else {
+        return load_raw<BYTES>(p);
+    }
 }
 
 template <uint32_t BYTES>
 __device__ inline void store_raw(uint8_t* p, typename Raw<BYTES>::type v)
 {
-    __builtin_memcpy(BYTES > 2 ? __builtin_assume_aligned(p, 2) : p, &v, BYTES);
+    if constexpr (BYTES == 16) __builtin_nontemporal_store(Quad{v.x, v.y, v.z, v.w}, reinterpret_cast<Quad*>(p));
+    else *reinterpret_cast<typename Raw<BYTES>::type*>(p) = v;
 }
 
 __device__ inline uint32_t bf16_rne(float f)
@@ -315,77 +336,94 @@ __device__ inline RowShape shape_of(const RowsArgs& a)
 constexpr uint32_t kRowThreads = 256;
 constexpr uint32_t kRowWaves = kRowThreads / 64;
 
-// The slot of choice k of a token, -1 if it is dropped or out of range.
-__device__ inline int32_t slot_of(const RowsArgs& a, uint64_t token, uint32_t k)
-{
-    const int32_t s = a.slots[token * a.top_k + k];
-    if (s >= int32_t(a.nrows)) {
-        set_status(a.status, ZIPCCL_STATUS_BAD_INDEX);
-        return -1;
-    }
-    return s < 0 ? -1 : s;
-}
+// Slot and weight of the choices of one token: lane k holds choice k (kMaxTopK lanes), -1
+// for one that is dropped or out of range.
+struct Choices {
+    int32_t slot = -1;
+    float weight = 1.0f;
 
-// A wave copies kC chunks per lane of one token's row to every slot of the token: the
-// row is read once whatever top_k is.
-template <uint32_t BYTES, uint32_t kC>
+    __device__ inline Choices(const RowsArgs& a, uint64_t token)
+    {
+        const uint32_t k = lane_id();
+        if (k >= a.top_k) return;
+        slot = a.slots[token * a.top_k + k];
+        if (a.weights) weight = a.weights[token * a.top_k + k];
+        if (slot >= int32_t(a.nrows)) {
+            set_status(a.status, ZIPCCL_STATUS_BAD_INDEX);
+            slot = -1;
+        }
+    }
+
+    __device__ inline int32_t slot_at(uint32_t k) const { return __builtin_amdgcn_readlane(slot, k); }
+    __device__ inline float weight_at(uint32_t k) const
+    {
+        return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weight), k));
+    }
+};
+static_assert(kMaxTopK <= 64, "a lane per choice");
+
+// Lanes past a row's end repeat its last chunk (one address, one value) rather than leave:
+// lane k's choice is read by the others at any place of the row.
+
+// Choices whose rows are in flight together.
+constexpr uint32_t kAhead = 4;
+
+// A wave takes one 16-byte chunk per lane of a token's row (1 KB; 2 and 4 KB per wave were
+// slower, 350 and 369 us against 347 for the dispatch of 16384 x 7168 to 8 rows each) and
+// copies it to every slot of the token: the row is read once whatever top_k is.
+template <uint32_t BYTES>
 __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(const RowsArgs a)
 {
     const RowShape sh = shape_of<BYTES>(a);
-    const uint32_t c0 = blockIdx.x * 64 * kC + lane_id();
+    const uint32_t c = min(blockIdx.x * 64 + lane_id(), sh.chunks - 1);
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     for (uint64_t token = uint64_t(blockIdx.y) * kRowWaves + wave; token < a.tokens;
          token += uint64_t(gridDim.y) * kRowWaves) {
-        const uint8_t* src = a.src + token * a.src_stride;
-        typename Raw<BYTES>::type v[kC];
-#pragma unroll
-        for (uint32_t j = 0; j < kC; j++)
-            if (c0 + 64 * j < sh.chunks) v[j] = load_raw<BYTES>(src + sh.at<BYTES>(c0 + 64 * j));
+        const uint32_t at = sh.at<BYTES>(c);
+        const auto v = load_kept<BYTES>(a.src + token * a.src_stride + at);   // on its way while the slots are looked up
+        const Choices choices(a, token);
         for (uint32_t k = 0; k < a.top_k; k++) {
-            const int32_t s = slot_of(a, token, k);
-            if (s < 0) continue;
-            uint8_t* dst = a.dst + uint64_t(uint32_t(s)) * a.dst_stride;
-#pragma unroll
-            for (uint32_t j = 0; j < kC; j++)
-                if (c0 + 64 * j < sh.chunks) store_raw<BYTES>(dst + sh.at<BYTES>(c0 + 64 * j), v[j]);
+            const int32_t s = choices.slot_at(k);
+            if (s >= 0) store_raw<BYTES>(a.dst + uint64_t(uint32_t(s)) * a.dst_stride + at, v);
         }
     }
 }
 
-// A wave sums kC chunks per lane of a token's rows, in the order of its choices, and
+// A wave sums one chunk per lane of a token's rows, in the order of its choices, and
 // rounds once.
-template <bool FP32, uint32_t BYTES, uint32_t kC>
+template <bool FP32, uint32_t BYTES>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(const RowsArgs a)
 {
     typedef Chunk<FP32, BYTES> Values;
     const RowShape sh = shape_of<BYTES>(a);
-    const uint32_t c0 = blockIdx.x * 64 * kC + lane_id();
+    const uint32_t c = min(blockIdx.x * 64 + lane_id(), sh.chunks - 1);
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     for (uint64_t token = uint64_t(blockIdx.y) * kRowWaves + wave; token < a.tokens;
          token += uint64_t(gridDim.y) * kRowWaves) {
-        Values acc[kC];
+        const Choices choices(a, token);
+        const uint32_t at = sh.at<BYTES>(c);
+        Values acc;
 #pragma unroll
-        for (uint32_t j = 0; j < kC; j++)
+        for (uint32_t i = 0; i < Values::kValues; i++) acc.v[i] = 0.0f;
+        for (uint32_t k0 = 0; k0 < a.top_k; k0 += kAhead) {
+            typename Raw<BYTES>::type raw[kAhead];
+            int32_t s[kAhead];
 #pragma unroll
-            for (uint32_t i = 0; i < Values::kValues; i++) acc[j].v[i] = 0.0f;
-        for (uint32_t k = 0; k < a.top_k; k++) {
-            const int32_t s = slot_of(a, token, k);
-            if (s < 0) continue;
-            const float w = a.weights ? a.weights[token * a.top_k + k] : 1.0f;
-            const uint8_t* src = a.src + uint64_t(uint32_t(s)) * a.src_stride;
+            for (uint32_t k = 0; k < kAhead; k++) {
+                s[k] = k0 + k < a.top_k ? choices.slot_at(k0 + k) : -1;
+                if (s[k] >= 0) raw[k] = load_raw<BYTES>(a.src + uint64_t(uint32_t(s[k])) * a.src_stride + at);
+            }
 #pragma unroll
-            for (uint32_t j = 0; j < kC; j++)
-                if (c0 + 64 * j < sh.chunks) {
-                    Values x;
-                    x.unpack(load_raw<BYTES>(src + sh.at<BYTES>(c0 + 64 * j)));
+            for (uint32_t k = 0; k < kAhead; k++) {
+                if (s[k] < 0) continue;
+                const float w = choices.weight_at(k0 + k);
+                Values x;
+                x.unpack(raw[k]);
 #pragma unroll
-                    for (uint32_t i = 0; i < Values::kValues; i++) acc[j].v[i] = fmaf(w, x.v[i], acc[j].v[i]);
-                }
+                for (uint32_t i = 0; i < Values::kValues; i++) acc.v[i] = fmaf(w, x.v[i], acc.v[i]);
+            }
         }
-        uint8_t* dst = a.dst + token * a.dst_stride;
-#pragma unroll
-        for (uint32_t j = 0; j < kC; j++)
-            if (c0 + 64 * j < sh.chunks) store_raw<BYTES>(dst + sh.at<BYTES>(c0 + 64 * j), acc[j].pack());
+        store_raw<BYTES>(a.dst + token * a.dst_stride + at, acc.pack());
     }
 }
 
@@ -395,60 +433,86 @@ __device__ inline float wave_sum(float v)
     return v;
 }
 
-// One workgroup per token: each choice's row is read for the weight's gradient
+// kWaves waves per token: each choice's row is read for the weight's gradient
 // <grad[token], y[slot]> and written with weight * grad[token].  Lane sums are joined by
-// a fixed tree over lanes, then waves.
-template <bool FP32, uint32_t BYTES>
+// a fixed tree over lanes, then in the order of the waves.
+template <bool FP32, uint32_t BYTES, uint32_t kWaves>
 __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(const RowsArgs a)
 {
     typedef Chunk<FP32, BYTES> Values;
+    constexpr uint32_t kTokens = kRowWaves / kWaves;   // of a workgroup
     __shared__ float s_dot[kMaxTopK][kRowWaves];
     const RowShape sh = shape_of<BYTES>(a);
-    const uint32_t tid = threadIdx.x, lane = lane_id();
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    for (uint64_t token = blockIdx.x; token < a.tokens; token += gridDim.x) {
-        const uint8_t* grad = a.grad + token * a.grad_stride;
-        for (uint32_t k = 0; k < a.top_k; k++) {
-            const int32_t s = slot_of(a, token, k);
-            float dot = 0.0f;
-            if (s >= 0) {
-                const float w = a.weights ? a.weights[token * a.top_k + k] : 1.0f;
-                const uint8_t* src = a.src + uint64_t(uint32_t(s)) * a.src_stride;
-                uint8_t* dst = a.dst + uint64_t(uint32_t(s)) * a.dst_stride;
-                for (uint32_t c = tid; c < sh.chunks; c += kRowThreads) {
+    const uint32_t lane = lane_id();
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), part = wave % kWaves;
+    for (uint64_t t0 = uint64_t(blockIdx.x) * kTokens; t0 < a.tokens; t0 += uint64_t(gridDim.x) * kTokens) {
+        const uint64_t token = t0 + wave / kWaves;
+        const bool have = token < a.tokens;
+        if (have) {
+            const Choices choices(a, token);
+            const uint8_t* grad = a.grad + token * a.grad_stride;
+            for (uint32_t k0 = 0; k0 < a.top_k; k0 += kAhead) {
+                int32_t s[kAhead];
+                float w[kAhead], dot[kAhead];
+#pragma unroll
+                for (uint32_t k = 0; k < kAhead; k++) {
+                    s[k] = k0 + k < a.top_k ? choices.slot_at(k0 + k) : -1;
+                    w[k] = choices.weight_at((k0 + k) & 63);
+                    dot[k] = 0.0f;
+                }
+                for (uint32_t c = 64 * part + lane; c < sh.chunks; c += 64 * kWaves) {
                     const uint32_t at = sh.at<BYTES>(c);
-                    Values g, y;
-                    g.unpack(load_raw<BYTES>(grad + at));
-                    y.unpack(load_raw<BYTES>(src + at));
                     // values of an overlapping last chunk that the chunk before it holds
                     const uint32_t skip = (c * BYTES - at) / (FP32 ? 4 : 2);
+                    Values g;
+                    typename Raw<BYTES>::type raw[kAhead];
+                    g.unpack(load_kept<BYTES>(grad + at));
 #pragma unroll
-                    for (uint32_t i = 0; i < Values::kValues; i++) {
-                        dot = i >= skip ? fmaf(g.v[i], y.v[i], dot) : dot;
-                        g.v[i] *= w;
+                    for (uint32_t k = 0; k < kAhead; k++)
+                        if (s[k] >= 0) raw[k] = load_raw<BYTES>(a.src + uint64_t(uint32_t(s[k])) * a.src_stride + at);
+#pragma unroll
+                    for (uint32_t k = 0; k < kAhead; k++) {
+                        if (s[k] < 0) continue;
+                        Values y, d;
+                        y.unpack(raw[k]);
+#pragma unroll
+                        for (uint32_t i = 0; i < Values::kValues; i++) {
+                            dot[k] = i >= skip ? fmaf(g.v[i], y.v[i], dot[k]) : dot[k];
+                            d.v[i] = g.v[i] * w[k];
+                        }
+                        store_raw<BYTES>(a.dst + uint64_t(uint32_t(s[k])) * a.dst_stride + at, d.pack());
                     }
-                    store_raw<BYTES>(dst + at, g.pack());
+                }
+#pragma unroll
+                for (uint32_t k = 0; k < kAhead; k++) {
+                    if (k0 + k >= a.top_k) break;
+                    const float sum = wave_sum(dot[k]);
+                    if (lane != 0) continue;
+                    if constexpr (kWaves == 1) a.grad_weights[token * a.top_k + k0 + k] = sum;
+                    else s_dot[k0 + k][wave] = sum;
                 }
             }
-            dot = wave_sum(dot);
-            if (lane == 0) s_dot[k][wave] = dot;
         }
-        __syncthreads();
-        if (tid < a.top_k) {
-            float dot = 0.0f;
-            for (uint32_t w = 0; w < kRowWaves; w++) dot += s_dot[tid][w];
-            a.grad_weights[token * a.top_k + tid] = dot;
+        if constexpr (kWaves > 1) {
+            static_assert(kWaves == kRowWaves, "one token per workgroup");
+            __syncthreads();
+            if (threadIdx.x < a.top_k) {
+                float dot = 0.0f;
+#pragma unroll
+                for (uint32_t v = 0; v < kWaves; v++) dot += s_dot[threadIdx.x][v];
+                a.grad_weights[token * a.top_k + threadIdx.x] = dot;
+            }
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 
 // Parts of a row in x (consecutive workgroups share a token), groups of tokens in y; the
 // kernels step over the tokens that a grid does not hold.
-dim3 grid_for(const RowsArgs& a, uint32_t unit, uint32_t chunks_per_lane)
+dim3 grid_for(const RowsArgs& a, uint32_t unit)
 {
     const uint64_t bytes = uint64_t(a.row_len) * (a.fp32 ? 4 : 2);
-    const uint64_t parts = ((bytes + unit - 1) / unit + 64 * chunks_per_lane - 1) / (64 * chunks_per_lane);
+    const uint64_t parts = ((bytes + unit - 1) / unit + 63) / 64;
     const uint64_t groups = (a.tokens + kRowWaves - 1) / kRowWaves;
     return dim3(uint32_t(parts), uint32_t(groups < 65535 ? groups : 65535));
 }
@@ -481,40 +545,40 @@ hipError_t launch_moe_sort(const SortArgs& a, hipStream_t s)
 
 hipError_t launch_moe_dispatch(const RowsArgs& a, hipStream_t s)
 {
-    const uint64_t bytes = uint64_t(a.row_len) * (a.fp32 ? 4 : 2);
     const dim3 block(kRowThreads);
-    if (bytes >= 16) hipLaunchKernelGGL((dispatch_kernel<16, 4>), grid_for(a, 16, 4), block, 0, s, a);
-    else if (a.fp32) hipLaunchKernelGGL((dispatch_kernel<4, 1>), grid_for(a, 4, 1), block, 0, s, a);
-    else hipLaunchKernelGGL((dispatch_kernel<2, 1>), grid_for(a, 2, 1), block, 0, s, a);
+    if (a.row_len * (a.fp32 ? 4ull : 2ull) >= 16) hipLaunchKernelGGL(dispatch_kernel<16>, grid_for(a, 16), block, 0, s, a);
+    else if (a.fp32) hipLaunchKernelGGL(dispatch_kernel<4>, grid_for(a, 4), block, 0, s, a);
+    else hipLaunchKernelGGL(dispatch_kernel<2>, grid_for(a, 2), block, 0, s, a);
     return hipGetLastError();
 }
 
 hipError_t launch_moe_combine(const RowsArgs& a, hipStream_t s)
 {
-    const uint64_t bytes = uint64_t(a.row_len) * (a.fp32 ? 4 : 2);
     const dim3 block(kRowThreads);
-    if (bytes >= 16) {
-        if (a.fp32) hipLaunchKernelGGL((combine_kernel<true, 16, 2>), grid_for(a, 16, 2), block, 0, s, a);
-        else hipLaunchKernelGGL((combine_kernel<false, 16, 2>), grid_for(a, 16, 2), block, 0, s, a);
+    if (a.row_len * (a.fp32 ? 4ull : 2ull) >= 16) {
+        if (a.fp32) hipLaunchKernelGGL((combine_kernel<true, 16>), grid_for(a, 16), block, 0, s, a);
+        else hipLaunchKernelGGL((combine_kernel<false, 16>), grid_for(a, 16), block, 0, s, a);
     } else if (a.fp32) {
-        hipLaunchKernelGGL((combine_kernel<true, 4, 1>), grid_for(a, 4, 1), block, 0, s, a);
+        hipLaunchKernelGGL((combine_kernel<true, 4>), grid_for(a, 4), block, 0, s, a);
     } else {
-        hipLaunchKernelGGL((combine_kernel<false, 2, 1>), grid_for(a, 2, 1), block, 0, s, a);
+        hipLaunchKernelGGL((combine_kernel<false, 2>), grid_for(a, 2), block, 0, s, a);
     }
     return hipGetLastError();
 }
 
 hipError_t launch_moe_combine_backward(const RowsArgs& a, hipStream_t s)
 {
-    const uint64_t bytes = uint64_t(a.row_len) * (a.fp32 ? 4 : 2);
-    const dim3 grid(uint32_t(a.tokens < (1u << 20) ? a.tokens : 1u << 20)), block(kRowThreads);   // the kernel steps on
-    if (bytes >= 16) {
-        if (a.fp32) hipLaunchKernelGGL((combine_backward_kernel<true, 16>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((combine_backward_kernel<false, 16>), grid, block, 0, s, a);
-    } else {
-        if (a.fp32) hipLaunchKernelGGL((combine_backward_kernel<true, 4>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((combine_backward_kernel<false, 2>), grid, block, 0, s, a);
-    }
+    const uint64_t bytes = a.row_len * (a.fp32 ? 4ull : 2ull);
+    const auto run = [&](auto kernel, uint32_t tokens) {   // tokens of a workgroup
+        const uint64_t groups = (a.tokens + tokens - 1) / tokens;
+        hipLaunchKernelGGL(kernel, dim3(uint32_t(groups < (1u << 20) ? groups : 1u << 20)), dim3(kRowThreads), 0, s, a);
+    };
+    // a wave per token up to 2 KB a row (8192 tokens of 4 choices: 28 us against 31 with a
+    // workgroup each at 2 KB, 60 and 53 at 4 KB), with enough tokens to fill the GPU (64 of
+    // 8 choices, 2 KB: 7.9 and 6.0)
+    if (bytes < 16) a.fp32 ? run(combine_backward_kernel<true, 4, 1>, 4) : run(combine_backward_kernel<false, 2, 1>, 4);
+    else if (bytes <= 2048 && a.tokens >= 1024) a.fp32 ? run(combine_backward_kernel<true, 16, 1>, 4) : run(combine_backward_kernel<false, 16, 1>, 4);
+    else a.fp32 ? run(combine_backward_kernel<true, 16, 4>, 1) : run(combine_backward_kernel<false, 16, 4>, 1);
     return hipGetLastError();
 }
 
