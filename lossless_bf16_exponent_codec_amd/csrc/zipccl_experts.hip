@@ -62,70 +62,131 @@ __device__ inline uint4 load8(const uint16_t* row, uint32_t h, uint32_t len)
     return v;
 }
 
-// Largest magnitude of 8 values as BF16 bits without sign (bits order as magnitudes do,
-// infinities and NaNs above every finite value).
-__device__ inline uint32_t peak_of(uint4 v)
+// Running maximum, in both halves, of magnitudes as BF16 bits without sign (bits order as
+// magnitudes do, infinities and NaNs above every finite value).
+typedef uint16_t Half2 __attribute__((ext_vector_type(2)));
+
+__device__ inline Half2 larger(Half2 m, uint4 v)
 {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 4; j++) m = max(m, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+    for (int j = 0; j < 4; j++) m = __builtin_elementwise_max(m, __builtin_bit_cast(Half2, w[j] & 0x7FFF7FFFu));
     return m;
 }
 
-// q of 8 values.  The row is scaled by a power of two that brings its peak into [1, 2)
-// (exact; values that underflow on the way quantise to 0 in any case), where the quotient
-// needs no care for range: reciprocal, product, and one correction by the remainder.
-__device__ inline uint2 quantize8(uint4 v, int exponent, float peak, float inverse)
-{
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t q[2] = {0, 0};
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-        const float x = __uint_as_float(j & 1 ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
-        const float n = 127.0f * ldexpf(x, exponent);
-        const float y = n * inverse;
-        const float z = fmaf(fmaf(-y, peak, n), inverse, y);
-        q[j >> 2] |= (uint32_t(int(rintf(z))) & 0xFFu) << (8 * (j & 3));
-    }
-    return make_uint2(q[0], q[1]);
-}
+// How a row of largest magnitude `most` is scaled.  n = x * up * factor is 127 x times the
+// power of two that brings `most` into [1, 2), exact (15 significant bits; values that
+// underflow on the way quantise to 0 in any case); `up` is 2^64 for rows so small that
+// the factor alone would overflow.
+struct RowScale {
+    float up = 1.0f, factor = 0.0f, peak = 1.0f, inverse = 0.0f, scale;
 
+    __device__ inline RowScale(uint32_t most_bits)
+    {
+        const float most = __uint_as_float(most_bits << 16);
+        scale = most_bits < 0x7F80u ? most / 127.0f : __uint_as_float(0x7FC00000u);
+        if (most_bits == 0 || most_bits >= 0x7F80u) return;   // q = 0
+        int e;
+        peak = 2.0f * frexpf(most, &e);
+        inverse = 1.0f / peak;
+        if (e < -100) {
+            up = 0x1p64f;
+            e += 64;
+        }
+        factor = ldexpf(127.0f, 1 - e);
+    }
+
+    // The quotient n / peak to the nearest fp32 (reciprocal, product, one correction by
+    // the remainder), then to the nearest even whole number by adding 1.5 * 2^23, whose
+    // low byte is then q's.
+    __device__ inline uint32_t quantize(float x) const
+    {
+        const float n = x * factor, y = n * inverse;
+        return __float_as_uint(fmaf(fmaf(-y, peak, n), inverse, y) + 12582912.0f);
+    }
+
+    __device__ inline uint2 quantize8(uint4 v) const
+    {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t q[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            float x = __uint_as_float(j & 1 ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
+            // a NaN or infinity has no place in a row that is not zeroed; the row's factor is 0 then
+            if (up != 1.0f) x *= up;
+            q[j] = quantize(x);
+        }
+        // low bytes of four: pairs, then pairs of pairs
+        const auto four = [](const uint32_t* b) {
+            return __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0C0C0400u),
+                                         __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u), 0x05040100u);
+        };
+        return make_uint2(four(q), four(q + 4));
+    }
+};
+
+// A group of kWaves waves per token.  kHeld: chunks of 8 values per lane that stay in
+// registers between the maximum and the quantisation (the row is read once); 0: rows of
+// any length, read twice.
+template <uint32_t kWaves, uint32_t kHeld>
 __global__ __launch_bounds__(kQuantThreads) void quantize_rows_kernel(const QuantArgs a)
 {
+    constexpr uint32_t kTokens = kQuantWaves / kWaves, kStride = 8 * 64 * kWaves;
     __shared__ uint32_t s_peak[kQuantWaves];
-    const uint32_t tid = threadIdx.x, lane = lane_id();
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t lane = lane_id();
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t first = 8 * (64 * (wave % kWaves) + lane);
     const uint32_t padded = (a.row_len + kQuantPad - 1) / kQuantPad * kQuantPad;
-    for (uint64_t token = blockIdx.x; token < a.tokens; token += gridDim.x) {
+    for (uint64_t t0 = uint64_t(blockIdx.x) * kTokens; t0 < a.tokens; t0 += uint64_t(gridDim.x) * kTokens) {
+        const uint64_t token = t0 + wave / kWaves;
+        if (kWaves == 1 && token >= a.tokens) break;
         const uint16_t* row = a.x + token * a.x_stride;
-        uint32_t m = 0;
-        for (uint32_t h = 8 * tid; h < a.row_len; h += 8 * kQuantThreads) m = max(m, peak_of(load8(row, h, a.row_len)));
-        for (uint32_t d = 32; d > 0; d >>= 1) m = max(m, uint32_t(__shfl_xor(int(m), int(d))));
-        __syncthreads();
-        if (lane == 0) s_peak[wave] = m;
-        __syncthreads();
-        for (uint32_t w = 0; w < kQuantWaves; w++) m = max(m, s_peak[w]);
-        const bool finite = m < 0x7F80u;
-        const float most = __uint_as_float(m << 16);
-        const float scale = finite ? most / 127.0f : __uint_as_float(0x7FC00000u);
-        const bool zero = m == 0 || !finite;
-        int e = 0;
-        const float peak = zero ? 1.0f : 2.0f * frexpf(most, &e);
-        const float inverse = 1.0f / peak;
-        for (uint32_t h = 8 * tid; h < padded; h += 8 * kQuantThreads) {
-            const uint2 q = zero ? make_uint2(0, 0) : quantize8(load8(row, h, a.row_len), 1 - e, peak, inverse);
+        uint4 held[kHeld > 0 ? kHeld : 1];
+        Half2 both = {0, 0};
+        if constexpr (kHeld > 0) {
+#pragma unroll
+            for (uint32_t j = 0; j < kHeld; j++) held[j] = load8(row, first + j * kStride, a.row_len);
+        }
+        // lane k: slot of choice k (kMaxTopK lanes)
+        int32_t slot = a.slots || lane > 0 ? -1 : int32_t(token);
+        if (a.slots && lane < a.top_k) slot = a.slots[token * a.top_k + lane];
+        if (slot >= int32_t(a.nrows)) {
+            set_status(a.status, ZIPCCL_STATUS_BAD_INDEX);
+            slot = -1;
+        }
+        if constexpr (kHeld > 0) {
+#pragma unroll
+            for (uint32_t j = 0; j < kHeld; j++) both = larger(both, held[j]);
+        } else {
+            for (uint32_t h = first; h < a.row_len; h += kStride) both = larger(both, load8(row, h, a.row_len));
+        }
+        uint32_t most = max(both.x, both.y);
+        for (uint32_t d = 32; d > 0; d >>= 1) most = max(most, uint32_t(__shfl_xor(int(most), int(d))));
+        if constexpr (kWaves > 1) {
+            __syncthreads();
+            if (lane == 0) s_peak[wave] = most;
+            __syncthreads();
+#pragma unroll
+            for (uint32_t w = 0; w < kQuantWaves; w++) most = max(most, s_peak[w]);
+        }
+        const bool zero = most == 0 || most >= 0x7F80u;
+        const RowScale to(__builtin_amdgcn_readfirstlane(most));
+        const auto put = [&](uint32_t h, uint4 v) {
+            const uint2 q = zero ? make_uint2(0, 0) : to.quantize8(v);
             for (uint32_t k = 0; k < a.top_k; k++) {
-                const int32_t s = a.slots ? a.slots[token * a.top_k + k] : int32_t(token);
-                if (s < 0 || s >= int32_t(a.nrows)) continue;
-                *reinterpret_cast<uint2*>(a.q + uint64_t(uint32_t(s)) * a.q_stride + h) = q;
+                const int32_t s = __builtin_amdgcn_readlane(slot, k);
+                if (s < 0) continue;
+                uint8_t* at = reinterpret_cast<uint8_t*>(a.q) + uint64_t(uint32_t(s)) * a.q_stride + h;
+                if (h < padded) *reinterpret_cast<uint2*>(at) = q;
             }
+        };
+        if constexpr (kHeld > 0) {
+#pragma unroll
+            for (uint32_t j = 0; j < kHeld; j++) put(first + j * kStride, held[j]);
+        } else {
+            for (uint32_t h0 = 0; h0 < padded; h0 += kStride) put(first + h0, load8(row, first + h0, a.row_len));
         }
-        if (tid < a.top_k) {
-            const int32_t s = a.slots ? a.slots[token * a.top_k + tid] : int32_t(token);
-            if (s >= int32_t(a.nrows)) set_status(a.status, ZIPCCL_STATUS_BAD_INDEX);
-            else if (s >= 0) a.scales[s] = scale;
-        }
+        if (wave % kWaves == 0 && slot >= 0) a.scales[slot] = to.scale;
     }
 }
 
@@ -591,8 +652,14 @@ uint64_t most_tiles(const ProductArgs& a, uint32_t per_tile)
 
 hipError_t launch_quantize_rows(const QuantArgs& a, hipStream_t s)
 {
-    const dim3 grid(uint32_t(a.tokens < (1u << 20) ? a.tokens : 1u << 20));   // the kernel steps on
-    hipLaunchKernelGGL(quantize_rows_kernel, grid, dim3(kQuantThreads), 0, s, a);
+    const auto run = [&](auto kernel, uint32_t tokens) {   // tokens of a workgroup
+        const uint64_t groups = (a.tokens + tokens - 1) / tokens;
+        hipLaunchKernelGGL(kernel, dim3(uint32_t(groups < (1u << 20) ? groups : 1u << 20)), dim3(kQuantThreads), 0, s, a);
+    };
+    const uint32_t padded = (a.row_len + kQuantPad - 1) / kQuantPad * kQuantPad;
+    if (padded <= 2048 && a.tokens >= 1024) run(quantize_rows_kernel<1, 4>, 4);
+    else if (padded <= 4 * 2048) run(quantize_rows_kernel<4, 4>, 1);
+    else run(quantize_rows_kernel<4, 0>, 1);
     return hipGetLastError();
 }
 
