@@ -478,7 +478,7 @@ zipccl_status zipccl_quantize_rows(const void* x, uint64_t x_stride, uint64_t to
 /* The experts' product in 8-bit integers: for the rows s of expert e (offsets[e] <= s <
  * offsets[e + 1]) and n < outputs
  *   out[s][n] = float(sum over h of q[s][h] * w[e][n][h]) * scales[s] * w_scales[e][n]
- * with exact 32-bit sums, rounded once to out_dtype.
+ * with exact 32-bit sums, rounded once to out_dtype (a NaN scale gives NaN).
  *   q, scales     rows as zipccl_quantize_rows writes them (q_stride bytes, zero-padded)
  *   w             device, num_experts * outputs rows of w_stride bytes in the same layout
  *   w_scales      device fp32[num_experts * outputs]

@@ -28,16 +28,12 @@ __device__ inline void set_status(uint32_t* status, uint32_t bits)
     if (status) atomicOr(status, bits);
 }
 
-// Two values rounded to BF16 (to nearest even), NaN as 0x7FC0.
+// Two values rounded to BF16 (to nearest even).
 __device__ inline uint32_t bf16_pair(float lo, float hi)
 {
     typedef float f2 __attribute__((ext_vector_type(2)));
     typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-    const f2 v = {lo == lo ? lo : __uint_as_float(0x7FC00000u), hi == hi ? hi : __uint_as_float(0x7FC00000u)};
-    const b2 b = __builtin_convertvector(v, b2);
-    uint32_t r;
-    __builtin_memcpy(&r, &b, 4);
-    return r;
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{lo, hi}), b2));
 }
 
 // ------------------------------------------------------------------------------------
