@@ -10,6 +10,8 @@
 // which tiles and waves add them does not show.
 #include <hip/hip_runtime.h>
 
+#include <atomic>
+
 #include "zipccl.h"
 #include "zipccl_moe_internal.h"
 
@@ -396,13 +398,16 @@ __device__ inline void product_tile(const ProductArgs& a, uint8_t* s_ring, uint3
     const uint32_t half = lane >> 5, turn = (lane >> 1) & 7;
     const uint8_t* read_q = s_ring + (wm + (lane & 31)) * kSlab;
     const uint8_t* read_w = s_ring + (kRows + wn + (lane & 31)) * kSlab;
+    // Quarters of a slab (32 values) that a set of registers holds: two, or all four (one
+    // barrier per slab) where the tile is small and the ring deep enough.
+    constexpr uint32_t kHeld = kM * kN > 4 || kSlots < 3 ? 2 : 4;
     v16i acc[kM][kN] = {};
-    v4i fq[2][2][kM], fw[2][2][kN];
-    const auto read = [&](uint32_t to, uint32_t slab) {   // half `to` of a slab into registers `to`
+    v4i fq[2][kHeld][kM], fw[2][kHeld][kN];
+    const auto read = [&](uint32_t to, uint32_t slab, uint32_t first) {   // quarters first .. into registers `to`
         const uint32_t slot = slab % kSlots * kSlot;
 #pragma unroll
-        for (uint32_t k = 0; k < 2; k++) {
-            const uint32_t at = slot + ((4 * to + 2 * k + half) ^ turn) * 16;
+        for (uint32_t k = 0; k < kHeld; k++) {
+            const uint32_t at = slot + ((2 * (first + k) + half) ^ turn) * 16;
 #pragma unroll
             for (uint32_t i = 0; i < kM; i++) fq[to][k][i] = *reinterpret_cast<const v4i*>(read_q + at + 32 * kSlab * i);
 #pragma unroll
@@ -425,25 +430,45 @@ __device__ inline void product_tile(const ProductArgs& a, uint8_t* s_ring, uint3
     const uint32_t n = n0 + wn + 8 * (lane % kPerRow);   // the 8 outputs it stores of each row
     const Outputs to(a, expert, n);
     wait_loads_and_meet<(kSlots - 1) * kLoads>();
-    read(0, 0);
-    for (uint32_t s = 0; s < a.slabs; s++) {
-        read(1, s);
-        multiply(0, 0);
-        take_turns<kProducts / 2 + 1, kLoads, 0x100>();
-        __builtin_amdgcn_sched_barrier(0);
-        wait_reads_and_meet();
-        load(s + kSlots, 0, kEarly);
-        multiply(0, 1);
-        take_turns<kProducts, kEarly, 0x020>();
-        __builtin_amdgcn_sched_barrier(0);
-        wait_loads_and_meet<(kSlots - 2) * kLoads + kEarly>();
-        load(s + kSlots, kEarly, kLoads);
-        read(0, s + 1);
-        multiply(1, 0);
-        multiply(1, 1);
-        take_turns<kProducts, kLoads - kEarly, 0x020>();
-        take_turns<kProducts / 2 + 1, kLoads, 0x100>();
-        __builtin_amdgcn_sched_barrier(0);
+    read(0, 0, 0);
+    if constexpr (kHeld == 4) {
+        for (uint32_t s0 = 0; s0 < a.slabs; s0 += 2) {
+#pragma unroll
+            for (uint32_t u = 0; u < 2; u++) {
+                const uint32_t s = s0 + u;
+                // slab s is in every wave's registers, slab s + 1 has landed
+                wait_loads_and_meet<(kSlots - 2) * kLoads>();
+                if (s >= a.slabs) break;
+                read(u ^ 1, s + 1, 0);
+                load(s + kSlots, 0, kLoads);
+#pragma unroll
+                for (uint32_t k = 0; k < 4; k++) multiply(u, k);
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                take_turns<2 * kProducts, 4 * (kM + kN), 0x100>();
+                take_turns<2 * kProducts, kLoads, 0x020>();
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    } else {
+        for (uint32_t s = 0; s < a.slabs; s++) {
+            read(1, s, 2);
+            multiply(0, 0);
+            take_turns<kProducts / 2 + 1, kLoads, 0x100>();
+            __builtin_amdgcn_sched_barrier(0);
+            wait_reads_and_meet();
+            load(s + kSlots, 0, kEarly);
+            multiply(0, 1);
+            take_turns<kProducts, kEarly, 0x020>();
+            __builtin_amdgcn_sched_barrier(0);
+            wait_loads_and_meet<(kSlots - 2) * kLoads + kEarly>();
+            load(s + kSlots, kEarly, kLoads);
+            read(0, s + 1, 0);
+            multiply(1, 0);
+            multiply(1, 1);
+            take_turns<kProducts, kLoads - kEarly, 0x020>();
+            take_turns<kProducts / 2 + 1, kLoads, 0x100>();
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
 
     // Lane l holds, of each 32 x 32 piece, row l % 32 and outputs 8 g + 4 (l / 32) .. + 3.
@@ -533,7 +558,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void product_large_kernel(const Pr
         return;
     }
     const uint32_t r = 128 * (p & 1), n0 = 256 * column + 64 * (p & 2);
-    if (r < rows && n0 < a.outputs) product_tile<2, 2, 2>(a, s_ring, expert, row0 + r, min(rows - r, 128u), n0);
+    if (r < rows && n0 < a.outputs) product_tile<2, 2, 4>(a, s_ring, expert, row0 + r, min(rows - r, 128u), n0);
 }
 
 // A tile of up to 64 rows x 32 outputs per workgroup, the row length split over its 4
@@ -661,11 +686,22 @@ hipError_t launch_quantize_rows(const QuantArgs& a, hipStream_t s)
 
 namespace {
 
-// Allows a kernel the LDS its launch asks for (past the 64 KB a launch has by default).
-hipError_t allow_lds(const void* kernel, uint32_t bytes)
+// Allows a kernel the LDS its launch asks for (past the 64 KB a launch has by default),
+// once per device: the call costs as much as the checks of a launch.
+template <auto kKernel>
+hipError_t allow_lds(uint32_t bytes)
 {
-    return bytes > 65536 ? hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, int(bytes))
-                         : hipSuccess;
+    static std::atomic<uint64_t> done{0};   // a bit per device
+    if (bytes <= 65536) return hipSuccess;
+    int device = 0;
+    if (hipError_t e = hipGetDevice(&device)) return e;
+    const uint64_t bit = device < 64 ? 1ull << device : 0;
+    if (done.load(std::memory_order_acquire) & bit) return hipSuccess;
+    if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kKernel),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, int(bytes)))
+        return e;
+    done.fetch_or(bit, std::memory_order_release);
+    return hipSuccess;
 }
 
 uint64_t columns(const ProductArgs& a, uint32_t outs) { return (a.outputs + outs - 1) / outs; }
@@ -680,9 +716,8 @@ template <uint32_t kM, uint32_t kN, uint32_t kSlots, uint32_t kPerCu>
 hipError_t launch_tiles(const ProductArgs& a, hipStream_t s)
 {
     constexpr uint32_t lds = tile_lds(kM, kN, kSlots);
-    const auto kernel = product_tile_kernel<kM, kN, kSlots, kPerCu>;
-    if (hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), lds)) return e;
-    hipLaunchKernelGGL(kernel, dim3(uint32_t(tile_workgroups<kM, kN>(a))), dim3(kTileThreads), lds, s, a);
+    if (hipError_t e = allow_lds<product_tile_kernel<kM, kN, kSlots, kPerCu>>(lds)) return e;
+    hipLaunchKernelGGL((product_tile_kernel<kM, kN, kSlots, kPerCu>), dim3(uint32_t(tile_workgroups<kM, kN>(a))), dim3(kTileThreads), lds, s, a);
     return hipGetLastError();
 }
 
@@ -739,14 +774,14 @@ hipError_t launch_experts_product(const ProductArgs& a, hipStream_t s)
         case Shape::wide: return launch_tiles<1, 2, 2, 3>(a, s);
         case Shape::square: return launch_tiles<2, 2, 2, 2>(a, s);
         case Shape::split: {
-            if (hipError_t e = allow_lds(reinterpret_cast<const void*>(product_split_kernel), kSplitLds)) return e;
+            if (hipError_t e = allow_lds<product_split_kernel>(kSplitLds)) return e;
             hipLaunchKernelGGL(product_split_kernel, dim3(uint32_t(split_workgroups(a))), dim3(kTileThreads), kSplitLds,
                                s, a);
             break;
         }
         case Shape::large: {
             constexpr uint32_t lds = tile_lds(4, 4, 2);
-            if (hipError_t e = allow_lds(reinterpret_cast<const void*>(product_large_kernel), lds)) return e;
+            if (hipError_t e = allow_lds<product_large_kernel>(lds)) return e;
             hipLaunchKernelGGL(product_large_kernel, dim3(uint32_t(large_workgroups(a))), dim3(kTileThreads), lds, s, a);
             break;
         }

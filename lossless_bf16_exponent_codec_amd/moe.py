@@ -1,0 +1,117 @@
+"""A mixture-of-experts layer's row traffic around the codec, from torch: a router's choices
+sorted by expert, tokens dispatched to their experts' rows and combined back with weights
+(differentiable), and experts' weights in 8 bits.
+
+Each step is one call of the same name in `zipccl`; this module adds the buffers and the
+gradients.  `examples/moe_exchange.py` runs the whole path, the compressed exchange
+between ranks included.
+"""
+from __future__ import annotations
+
+from dataclasses import dataclass
+
+import torch
+
+from . import zipccl as Z
+
+__all__ = ["Routing", "route", "dispatch", "combine", "QuantizedRows", "quantize", "QuantizedExperts"]
+
+
+@dataclass
+class Routing:
+    """Choices sorted by expert: rows[offsets[e]:offsets[e + 1]] are the tokens of expert
+    e's rows, slots[t, k] the row of token t's k-th choice (-1: dropped)."""
+    offsets: torch.Tensor
+    rows: torch.Tensor
+    slots: torch.Tensor
+
+    def splits(self) -> list:
+        """The offsets on the host (waits for the sort): sizes of buffers and of the
+        all-to-all.  The last one is the number of rows."""
+        return self.offsets.tolist()
+
+
+def route(experts: torch.Tensor, num_experts: int, status=None) -> Routing:
+    """Sorts a router's choices (tokens x top_k expert numbers, negative ones dropped)."""
+    dev, i32 = experts.device, torch.int32
+    r = Routing(torch.empty(num_experts + 1, dtype=i32, device=dev), torch.empty(experts.numel(), dtype=i32, device=dev),
+                torch.empty(experts.shape, dtype=i32, device=dev))
+    space = torch.empty(Z.MOE_SORT_WORKSPACE_BYTES, dtype=torch.uint8, device=dev)
+    Z.moe_sort(experts, num_experts, r.offsets, r.rows, r.slots, space, status)
+    return r
+
+
+class _Dispatch(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, slots, nrows):
+        ctx.save_for_backward(slots)
+        y = x.new_empty(nrows, x.shape[1])
+        Z.moe_dispatch(x, slots, y)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        slots, = ctx.saved_tensors
+        dx = dy.new_empty(slots.shape[0], dy.shape[1])
+        Z.moe_dispatch_backward(dy.contiguous(), slots, dx)
+        return dx, None, None
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y, slots, weights):
+        ctx.save_for_backward(y, slots, weights)
+        out = y.new_empty(slots.shape[0], y.shape[1])
+        Z.moe_combine(y, slots, weights, out)
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        y, slots, weights = ctx.saved_tensors
+        dy, dw = torch.zeros_like(y), torch.empty_like(weights)   # zeros: rows that no choice names
+        Z.moe_combine_backward(dout.contiguous(), y, slots, weights, dy, dw)
+        return dy, None, dw
+
+
+def dispatch(x: torch.Tensor, routing: Routing, nrows: int) -> torch.Tensor:
+    """Rows by expert (nrows = routing.splits()[-1]) of the tokens x; differentiable in x."""
+    return _Dispatch.apply(x, routing.slots, nrows)
+
+
+def combine(y: torch.Tensor, routing: Routing, weights: torch.Tensor) -> torch.Tensor:
+    """Tokens from rows by expert: sums with weights (float32, tokens x top_k);
+    differentiable in y and weights."""
+    return _Combine.apply(y, routing.slots, weights.contiguous())
+
+
+@dataclass
+class QuantizedRows:
+    """8-bit rows (padded to a multiple of 128) and their scales."""
+    q: torch.Tensor
+    scales: torch.Tensor
+    row_len: int
+
+
+def quantize(x: torch.Tensor, slots=None, nrows: int | None = None) -> QuantizedRows:
+    """BF16 rows in 8 bits: row by row, or each token's to its slots among nrows rows."""
+    n, wide = x.shape[0] if slots is None else nrows, -(-x.shape[1] // Z.ROW_PAD) * Z.ROW_PAD
+    r = QuantizedRows(torch.empty(n, wide, dtype=torch.int8, device=x.device),
+                      torch.empty(n, dtype=torch.float32, device=x.device), x.shape[1])
+    Z.quantize_rows(x, r.q, r.scales, slots=slots)
+    return r
+
+
+class QuantizedExperts:
+    """Weights of all experts (experts x outputs x inputs, BF16) laid out once in 8 bits
+    with a scale per output channel.  Calling it multiplies rows sorted by expert."""
+
+    def __init__(self, weights: torch.Tensor):
+        self.experts, self.outputs, self.inputs = weights.shape
+        rows = quantize(weights.reshape(-1, self.inputs))
+        self.q = rows.q.view(self.experts, self.outputs, -1)
+        self.scales = rows.scales.view(self.experts, self.outputs)
+
+    def __call__(self, rows: QuantizedRows, routing: Routing, dtype=torch.bfloat16) -> torch.Tensor:
+        out = torch.empty(rows.q.shape[0], self.outputs, dtype=dtype, device=rows.q.device)
+        Z.experts_product(rows.q, rows.scales, self.q, self.scales, self.inputs, out, offsets=routing.offsets)
+        return out

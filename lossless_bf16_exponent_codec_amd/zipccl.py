@@ -166,7 +166,7 @@ def _ptr(t) -> int | None:
 def _stream(stream) -> int | None:
     if stream is None:
         # the handle alone: building a torch.cuda.Stream takes 3 us, as long as a launch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
