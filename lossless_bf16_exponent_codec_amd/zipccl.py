@@ -163,10 +163,13 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
 def _stream(stream) -> int | None:
     if stream is None:
         # the handle alone: building a torch.cuda.Stream takes 3 us, as long as a launch
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _raw_stream(_current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
