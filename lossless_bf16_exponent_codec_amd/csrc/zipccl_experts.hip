@@ -546,9 +546,10 @@ __global__ __launch_bounds__(kTileThreads, 1) void product_large_kernel(const Pr
     const uint32_t across = (a.outputs + 255) / 256, down = map.count(a), total = down * across;
     const uint32_t left = total % kCus;
     const uint32_t whole = left <= kCutTiles ? total - left : total;   // the tiles not cut
-    const bool cut = blockIdx.x >= whole;
+    const uint32_t first_cut = (whole + kXcds - 1) / kXcds * kXcds;    // the workgroups that share `whole` tiles
+    const bool cut = blockIdx.x >= first_cut;
     const uint32_t parts = 4 * (total - whole);
-    const uint32_t p = cut ? run_of_xcd(blockIdx.x - whole, parts) : run_of_xcd(blockIdx.x, whole);
+    const uint32_t p = cut ? run_of_xcd(blockIdx.x - first_cut, parts) : run_of_xcd(blockIdx.x, whole);
     if (p >= (cut ? parts : whole)) return;
     uint32_t row_tile, column, expert, row0, rows;
     tile_at(cut ? whole + p / 4 : p, down, across, row_tile, column);
@@ -728,9 +729,8 @@ uint64_t split_workgroups(const ProductArgs& a) { return most_tiles(a, 64) * col
 
 // Which kernel, by the tiles that rows spread evenly over the experts would make (the
 // host does not know the offsets).  Times in us, weights outputs x row_len:
-//  - one round of split workgroups or less: split (1 expert, 64 rows, 2048 x 7168: 9.2
-//    against 18.1 for 64 x 64 tiles; 4 experts: 15.2 and 19.3; 8 experts, two rounds: 29.9
-//    and 22.1);
+//  - one round of split workgroups or less: split (1 expert, 64 rows, 2048 x 7168: 9.7
+//    against 13.4 for 64 x 64 tiles; 8 experts, two rounds: 29.9 and 22.3);
 //  - up to 64 rows for an expert the weights' reads are what counts.  Few tiles of 64 x 64:
 //    four slabs deep while a CU has no second workgroup to run meanwhile (8 experts, 2048 x
 //    7168: 20 and 26 at two), else two slabs and four workgroups (16 experts: 35 and 35).
@@ -738,7 +738,9 @@ uint64_t split_workgroups(const ProductArgs& a) { return most_tiles(a, 64) * col
 //    experts, 2048 x 7168: 78 against 94 at 64 x 64; 1024 over 128: 279 and 286);
 //  - 256 x 256 from 192 rows on when there is a round of it (8 experts, 2048 rows each,
 //    2048 x 7168: 212 against 246 at 128 x 128; 512 rows each, half a round: 78 and 62);
-//  - else 128 x 128 (64 x 64 at 128 rows, 32 experts, 2048 x 7168: 148 and 105).
+//  - else 128 x 128 (32 experts, 128 rows each, 2048 x 7168: 105, 148 at 64 x 64), or 64 x
+//    128 where those would leave too many CUs idle (1 expert, 512 rows, 4096 x 2048, 128
+//    tiles: 12.3 and 10.0; 700 rows, 192 tiles: 12.8 and 14.3).
 enum class Shape { split, narrow_deep, narrow, wide, square, large };
 
 Shape choose(const ProductArgs& a)
@@ -750,7 +752,8 @@ Shape choose(const ProductArgs& a)
         const uint64_t n = tiles(64, 64);
         return n <= kCus + kCus / 2 ? Shape::narrow_deep : n <= 3 * kCus ? Shape::narrow : Shape::wide;
     }
-    return each >= 192 && tiles(256, 256) >= kCus ? Shape::large : Shape::square;
+    if (each >= 192 && tiles(256, 256) >= kCus) return Shape::large;
+    return tiles(128, 128) <= kCus * 5 / 8 ? Shape::wide : Shape::square;
 }
 
 }  // namespace
