@@ -535,9 +535,10 @@ __global__ __launch_bounds__(kTileThreads, kPerCu) void product_tile_kernel(cons
 }
 
 // Tiles of 256 x 256, one workgroup per CU.  Where the tiles past the last whole round of
-// the 256 CUs are few, each is cut into four of 128 x 128, so that the last round takes a
-// part of a tile's time.
-constexpr uint32_t kCus = 256, kCutTiles = kCus / 4;
+// the 256 CUs are half a round or less, each is cut into four of 128 x 128, so that the
+// last round takes a part of a tile's time (1 expert, 4096 x 7168: 352 tiles, 96 over, 167
+// us and 184 uncut; 1120 tiles, 96 over, 474 and 494).
+constexpr uint32_t kCus = 256, kCutTiles = kCus / 2;
 
 __global__ __launch_bounds__(kTileThreads, 1) void product_large_kernel(const ProductArgs a)
 {
