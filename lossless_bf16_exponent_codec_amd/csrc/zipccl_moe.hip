@@ -236,39 +236,36 @@ template <> struct Raw<16> { typedef uint4 type; };
 template <> struct Raw<4> { typedef uint32_t type; };
 template <> struct Raw<2> { typedef uint16_t type; };
 
-// The rows by expert, 8 times the tokens' bytes at 8 choices, are read and written with
-// non-temporal accesses; the tokens' rows, which fit the Infinity Cache where those do not,
-// with plain ones (16384 tokens of 7168 to 8 rows each: dispatch 346 us, 385 with plain
-// stores, 425 with non-temporal loads; combine 345 us, 400 with plain loads).
+// kStream: non-temporal accesses, for rows that do not fit the Infinity Cache (16384 tokens
+// of 7168 to 8 rows each, 1.9 GB: dispatch 343 us, 385 with plain stores; combine 345 us,
+// 400 with plain loads).  What fits is left to the caches (4096 tokens of 4098 to 4 rows
+// each, 168 MB: dispatch 26.4 us, 36.4 with non-temporal stores, whose lines at the ends of
+// rows are written in parts; combine 25.1 and 30.6).
 typedef uint32_t Quad __attribute__((ext_vector_type(4), aligned(2)));
 
-template <uint32_t BYTES>
+template <uint32_t BYTES, bool kStream>
 __device__ inline typename Raw<BYTES>::type load_raw(const uint8_t* p)
 {
     if constexpr (BYTES == 16) {
-        const Quad v = __builtin_nontemporal_load(reinterpret_cast<const Quad*>(p));
+        Quad v;
+        if constexpr (kStream) v = __builtin_nontemporal_load(reinterpret_cast<const Quad*>(p));
+        else v = *reinterpret_cast<const Quad*>(p);
         return make_uint4(v.x, v.y, v.z, v.w);
     } else {
         return *reinterpret_cast<const typename Raw<BYTES>::type*>(p);
     }
 }
 
-template <uint32_t BYTES>
-__device__ inline typename Raw<BYTES>::type load_kept(const uint8_t* p)
-{
-    if constexpr (BYTES == 16) {
-        const Quad v = *reinterpret_cast<const Quad*>(p);
-        return make_uint4(v.x, v.y, v.z, v.w);
-    } else {
-        return load_raw<BYTES>(p);
-    }
-}
-
-template <uint32_t BYTES>
+template <uint32_t BYTES, bool kStream>
 __device__ inline void store_raw(uint8_t* p, typename Raw<BYTES>::type v)
 {
-    if constexpr (BYTES == 16) __builtin_nontemporal_store(Quad{v.x, v.y, v.z, v.w}, reinterpret_cast<Quad*>(p));
-    else *reinterpret_cast<typename Raw<BYTES>::type*>(p) = v;
+    if constexpr (BYTES == 16) {
+        const Quad q = {v.x, v.y, v.z, v.w};
+        if constexpr (kStream) __builtin_nontemporal_store(q, reinterpret_cast<Quad*>(p));
+        else *reinterpret_cast<Quad*>(p) = q;
+    } else {
+        *reinterpret_cast<typename Raw<BYTES>::type*>(p) = v;
+    }
 }
 
 __device__ inline uint32_t bf16_rne(float f)
@@ -336,170 +333,193 @@ __device__ inline RowShape shape_of(const RowsArgs& a)
 constexpr uint32_t kRowThreads = 256;
 constexpr uint32_t kRowWaves = kRowThreads / 64;
 
-// Slot and weight of the choices of one token: lane k holds choice k (kMaxTopK lanes), -1
-// for one that is dropped or out of range.
-struct Choices {
-    int32_t slot = -1;
-    float weight = 1.0f;
-
-    __device__ inline Choices(const RowsArgs& a, uint64_t token)
-    {
-        const uint32_t k = lane_id();
-        if (k >= a.top_k) return;
-        slot = a.slots[token * a.top_k + k];
-        if (a.weights) weight = a.weights[token * a.top_k + k];
-        if (slot >= int32_t(a.nrows)) {
-            set_status(a.status, ZIPCCL_STATUS_BAD_INDEX);
-            slot = -1;
-        }
-    }
-
-    __device__ inline int32_t slot_at(uint32_t k) const { return __builtin_amdgcn_readlane(slot, k); }
-    __device__ inline float weight_at(uint32_t k) const
-    {
-        return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weight), k));
-    }
-};
-static_assert(kMaxTopK <= 64, "a lane per choice");
-
-// Lanes past a row's end repeat its last chunk (one address, one value) rather than leave:
-// lane k's choice is read by the others at any place of the row.
-
 // Choices whose rows are in flight together.
 constexpr uint32_t kAhead = 4;
 
-// A wave takes one 16-byte chunk per lane of a token's row (1 KB; 2 and 4 KB per wave were
-// slower, 350 and 369 us against 347 for the dispatch of 16384 x 7168 to 8 rows each) and
-// copies it to every slot of the token: the row is read once whatever top_k is.
-template <uint32_t BYTES>
+// Choices k0 .. k0 + kAhead - 1 of a token: slots (-1 for one that is dropped, out of range,
+// or past the last) and weights.
+struct Choices {
+    int32_t slot[kAhead];
+    float weight[kAhead];
+
+    __device__ inline Choices(const RowsArgs& a, uint64_t token, uint32_t k0)
+    {
+        const uint64_t at = token * a.top_k + k0;
+#pragma unroll
+        for (uint32_t k = 0; k < kAhead; k++) {
+            const bool have = k0 + k < a.top_k;
+            slot[k] = have ? a.slots[at + k] : -1;
+            weight[k] = have && a.weights ? a.weights[at + k] : 1.0f;
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < kAhead; k++) {
+            if (slot[k] < int32_t(a.nrows)) continue;
+            set_status(a.status, ZIPCCL_STATUS_BAD_INDEX);
+            slot[k] = -1;
+        }
+    }
+};
+
+// One chunk of a token's row to each of its slots: the row is read once whatever top_k is.
+template <uint32_t BYTES, bool kStream>
+__device__ inline void dispatch_chunk(const RowsArgs& a, uint64_t token, uint32_t at)
+{
+    const auto v = load_raw<BYTES, false>(a.src + token * a.src_stride + at);
+    for (uint32_t k0 = 0; k0 < a.top_k; k0 += kAhead) {
+        const Choices c(a, token, k0);
+#pragma unroll
+        for (uint32_t k = 0; k < kAhead; k++)
+            if (c.slot[k] >= 0) store_raw<BYTES, kStream>(a.dst + uint64_t(uint32_t(c.slot[k])) * a.dst_stride + at, v);
+    }
+}
+
+// One chunk of the weighted sum of a token's rows, in the order of its choices, rounded
+// once.
+template <bool FP32, uint32_t BYTES, bool kStream>
+__device__ inline void combine_chunk(const RowsArgs& a, uint64_t token, uint32_t at)
+{
+    typedef Chunk<FP32, BYTES> Values;
+    Values sum;
+#pragma unroll
+    for (uint32_t i = 0; i < Values::kValues; i++) sum.v[i] = 0.0f;
+    for (uint32_t k0 = 0; k0 < a.top_k; k0 += kAhead) {
+        const Choices c(a, token, k0);
+        typename Raw<BYTES>::type raw[kAhead];
+#pragma unroll
+        for (uint32_t k = 0; k < kAhead; k++)
+            if (c.slot[k] >= 0) raw[k] = load_raw<BYTES, kStream>(a.src + uint64_t(uint32_t(c.slot[k])) * a.src_stride + at);
+#pragma unroll
+        for (uint32_t k = 0; k < kAhead; k++) {
+            if (c.slot[k] < 0) continue;
+            Values x;
+            x.unpack(raw[k]);
+#pragma unroll
+            for (uint32_t i = 0; i < Values::kValues; i++) sum.v[i] = fmaf(c.weight[k], x.v[i], sum.v[i]);
+        }
+    }
+    store_raw<BYTES, kStream>(a.dst + token * a.dst_stride + at, sum.pack());
+}
+
+// Two ways of sharing the chunks out.
+//
+// By waves: a wave takes 64 consecutive chunks (1 KB) of one token, whose slots and
+// weights are then scalar values.  Parts of a row in x, so that consecutive workgroups
+// share a token, groups of tokens in y.  For rows that fill such parts (2 and 4 KB per
+// wave were slower: 350 and 369 us for the dispatch above).
+template <class Take>
+__device__ inline void by_waves(const RowsArgs& a, const RowShape& sh, Take&& take)
+{
+    const uint32_t c = blockIdx.x * 64 + lane_id();
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (c >= sh.chunks) return;
+    for (uint64_t token = uint64_t(blockIdx.y) * kRowWaves + wave; token < a.tokens;
+         token += uint64_t(gridDim.y) * kRowWaves)
+        take(token, sh.at<16>(c));
+}
+
+// By lanes: lane after lane through the chunks of token after token, for rows of any
+// length; each of the 8 XCDs (workgroups go to them in turn) takes a run of tokens, so
+// that lines that two rows or two workgroups share meet in one L2.  A slice of the tokens
+// in x, slices in y.
+template <uint32_t BYTES, class Take>
+__device__ inline void by_lanes(const RowsArgs& a, const RowShape& sh, Take&& take)
+{
+    const uint32_t block = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
+    const uint32_t i = block * kRowThreads + threadIdx.x;
+    const uint32_t in = uint32_t((uint64_t(i) * a.inverse) >> a.shift);   // token of the slice
+    if (in >= a.slice) return;
+    for (uint64_t token = uint64_t(blockIdx.y) * a.slice + in; token < a.tokens; token += uint64_t(gridDim.y) * a.slice)
+        take(token, sh.at<BYTES>(i - in * sh.chunks));
+}
+
+template <bool kWaves, uint32_t BYTES, bool kStream>
 __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(const RowsArgs a)
 {
     const RowShape sh = shape_of<BYTES>(a);
-    const uint32_t c = min(blockIdx.x * 64 + lane_id(), sh.chunks - 1);
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    for (uint64_t token = uint64_t(blockIdx.y) * kRowWaves + wave; token < a.tokens;
-         token += uint64_t(gridDim.y) * kRowWaves) {
-        const uint32_t at = sh.at<BYTES>(c);
-        const auto v = load_kept<BYTES>(a.src + token * a.src_stride + at);   // on its way while the slots are looked up
-        const Choices choices(a, token);
-        for (uint32_t k = 0; k < a.top_k; k++) {
-            const int32_t s = choices.slot_at(k);
-            if (s >= 0) store_raw<BYTES>(a.dst + uint64_t(uint32_t(s)) * a.dst_stride + at, v);
-        }
-    }
+    const auto take = [&](uint64_t token, uint32_t at) { dispatch_chunk<BYTES, kStream>(a, token, at); };
+    if constexpr (kWaves) by_waves(a, sh, take);
+    else by_lanes<BYTES>(a, sh, take);
 }
 
-// A wave sums one chunk per lane of a token's rows, in the order of its choices, and
-// rounds once.
-template <bool FP32, uint32_t BYTES>
+template <bool kWaves, bool FP32, uint32_t BYTES, bool kStream>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(const RowsArgs a)
 {
-    typedef Chunk<FP32, BYTES> Values;
     const RowShape sh = shape_of<BYTES>(a);
-    const uint32_t c = min(blockIdx.x * 64 + lane_id(), sh.chunks - 1);
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    for (uint64_t token = uint64_t(blockIdx.y) * kRowWaves + wave; token < a.tokens;
-         token += uint64_t(gridDim.y) * kRowWaves) {
-        const Choices choices(a, token);
-        const uint32_t at = sh.at<BYTES>(c);
-        Values acc;
-#pragma unroll
-        for (uint32_t i = 0; i < Values::kValues; i++) acc.v[i] = 0.0f;
-        for (uint32_t k0 = 0; k0 < a.top_k; k0 += kAhead) {
-            typename Raw<BYTES>::type raw[kAhead];
-            int32_t s[kAhead];
-#pragma unroll
-            for (uint32_t k = 0; k < kAhead; k++) {
-                s[k] = k0 + k < a.top_k ? choices.slot_at(k0 + k) : -1;
-                if (s[k] >= 0) raw[k] = load_raw<BYTES>(a.src + uint64_t(uint32_t(s[k])) * a.src_stride + at);
-            }
-#pragma unroll
-            for (uint32_t k = 0; k < kAhead; k++) {
-                if (s[k] < 0) continue;
-                const float w = choices.weight_at(k0 + k);
-                Values x;
-                x.unpack(raw[k]);
-#pragma unroll
-                for (uint32_t i = 0; i < Values::kValues; i++) acc.v[i] = fmaf(w, x.v[i], acc.v[i]);
-            }
-        }
-        store_raw<BYTES>(a.dst + token * a.dst_stride + at, acc.pack());
-    }
+    const auto take = [&](uint64_t token, uint32_t at) { combine_chunk<FP32, BYTES, kStream>(a, token, at); };
+    if constexpr (kWaves) by_waves(a, sh, take);
+    else by_lanes<BYTES>(a, sh, take);
 }
 
-__device__ inline float wave_sum(float v)
+// Sum over groups of kLanes lanes.
+template <uint32_t kLanes>
+__device__ inline float lanes_sum(float v)
 {
-    for (uint32_t d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+#pragma unroll
+    for (uint32_t d = kLanes / 2; d > 0; d >>= 1) v += __shfl_xor(v, d);
     return v;
 }
 
-// kWaves waves per token: each choice's row is read for the weight's gradient
-// <grad[token], y[slot]> and written with weight * grad[token].  Lane sums are joined by
-// a fixed tree over lanes, then in the order of the waves.
-template <bool FP32, uint32_t BYTES, uint32_t kWaves>
+// kLanes lanes per token (a part of a wave, a wave, or all of the workgroup's): each
+// choice's row is read for the weight's gradient <grad[token], y[slot]> and written with
+// weight * grad[token].  Lane sums are joined by a fixed tree over lanes, then in the order
+// of the waves.
+template <bool FP32, uint32_t BYTES, uint32_t kLanes, bool kStream>
 __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(const RowsArgs a)
 {
     typedef Chunk<FP32, BYTES> Values;
-    constexpr uint32_t kTokens = kRowWaves / kWaves;   // of a workgroup
-    __shared__ float s_dot[kMaxTopK][kRowWaves];
+    constexpr bool kWide = kLanes == kRowThreads;
+    constexpr uint32_t kTokens = kRowThreads / kLanes;   // of a workgroup
+    __shared__ float s_dot[kWide ? kMaxTopK : 1][kRowWaves];
     const RowShape sh = shape_of<BYTES>(a);
-    const uint32_t lane = lane_id();
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), part = wave % kWaves;
+    const uint32_t part = threadIdx.x % kLanes;
     for (uint64_t t0 = uint64_t(blockIdx.x) * kTokens; t0 < a.tokens; t0 += uint64_t(gridDim.x) * kTokens) {
-        const uint64_t token = t0 + wave / kWaves;
-        const bool have = token < a.tokens;
-        if (have) {
-            const Choices choices(a, token);
-            const uint8_t* grad = a.grad + token * a.grad_stride;
-            for (uint32_t k0 = 0; k0 < a.top_k; k0 += kAhead) {
-                int32_t s[kAhead];
-                float w[kAhead], dot[kAhead];
+        // the last workgroup's groups past the last token repeat it
+        const uint64_t mine = t0 + threadIdx.x / kLanes, token = mine < a.tokens ? mine : a.tokens - 1;
+        const uint8_t* grad = a.grad + token * a.grad_stride;
+        for (uint32_t k0 = 0; k0 < a.top_k; k0 += kAhead) {
+            const Choices choice(a, token, k0);
+            float dot[kAhead] = {};
+            for (uint32_t c = part; c < sh.chunks; c += kLanes) {
+                const uint32_t at = sh.at<BYTES>(c);
+                // values of an overlapping last chunk that the chunk before it holds
+                const uint32_t skip = (c * BYTES - at) / (FP32 ? 4 : 2);
+                Values g;
+                typename Raw<BYTES>::type raw[kAhead];
+                g.unpack(load_raw<BYTES, false>(grad + at));
+#pragma unroll
+                for (uint32_t k = 0; k < kAhead; k++)
+                    if (choice.slot[k] >= 0)
+                        raw[k] = load_raw<BYTES, kStream>(a.src + uint64_t(uint32_t(choice.slot[k])) * a.src_stride + at);
 #pragma unroll
                 for (uint32_t k = 0; k < kAhead; k++) {
-                    s[k] = k0 + k < a.top_k ? choices.slot_at(k0 + k) : -1;
-                    w[k] = choices.weight_at((k0 + k) & 63);
-                    dot[k] = 0.0f;
-                }
-                for (uint32_t c = 64 * part + lane; c < sh.chunks; c += 64 * kWaves) {
-                    const uint32_t at = sh.at<BYTES>(c);
-                    // values of an overlapping last chunk that the chunk before it holds
-                    const uint32_t skip = (c * BYTES - at) / (FP32 ? 4 : 2);
-                    Values g;
-                    typename Raw<BYTES>::type raw[kAhead];
-                    g.unpack(load_kept<BYTES>(grad + at));
+                    if (choice.slot[k] < 0) continue;
+                    Values y, d;
+                    y.unpack(raw[k]);
 #pragma unroll
-                    for (uint32_t k = 0; k < kAhead; k++)
-                        if (s[k] >= 0) raw[k] = load_raw<BYTES>(a.src + uint64_t(uint32_t(s[k])) * a.src_stride + at);
-#pragma unroll
-                    for (uint32_t k = 0; k < kAhead; k++) {
-                        if (s[k] < 0) continue;
-                        Values y, d;
-                        y.unpack(raw[k]);
-#pragma unroll
-                        for (uint32_t i = 0; i < Values::kValues; i++) {
-                            dot[k] = i >= skip ? fmaf(g.v[i], y.v[i], dot[k]) : dot[k];
-                            d.v[i] = g.v[i] * w[k];
-                        }
-                        store_raw<BYTES>(a.dst + uint64_t(uint32_t(s[k])) * a.dst_stride + at, d.pack());
+                    for (uint32_t i = 0; i < Values::kValues; i++) {
+                        dot[k] = i >= skip ? fmaf(g.v[i], y.v[i], dot[k]) : dot[k];
+                        d.v[i] = g.v[i] * choice.weight[k];
                     }
+                    store_raw<BYTES, kStream>(a.dst + uint64_t(uint32_t(choice.slot[k])) * a.dst_stride + at, d.pack());
                 }
+            }
 #pragma unroll
-                for (uint32_t k = 0; k < kAhead; k++) {
-                    if (k0 + k >= a.top_k) break;
-                    const float sum = wave_sum(dot[k]);
-                    if (lane != 0) continue;
-                    if constexpr (kWaves == 1) a.grad_weights[token * a.top_k + k0 + k] = sum;
-                    else s_dot[k0 + k][wave] = sum;
+            for (uint32_t k = 0; k < kAhead; k++) {
+                if (k0 + k >= a.top_k) break;
+                const float sum = lanes_sum<kWide ? 64 : kLanes>(dot[k]);
+                if constexpr (kWide) {
+                    if (lane_id() == 0) s_dot[k0 + k][threadIdx.x >> 6] = sum;
+                } else {
+                    if (part == 0) a.grad_weights[token * a.top_k + k0 + k] = sum;
                 }
             }
         }
-        if constexpr (kWaves > 1) {
-            static_assert(kWaves == kRowWaves, "one token per workgroup");
+        if constexpr (kWide) {
             __syncthreads();
             if (threadIdx.x < a.top_k) {
                 float dot = 0.0f;
 #pragma unroll
-                for (uint32_t v = 0; v < kWaves; v++) dot += s_dot[threadIdx.x][v];
+                for (uint32_t v = 0; v < kRowWaves; v++) dot += s_dot[threadIdx.x][v];
                 a.grad_weights[token * a.top_k + threadIdx.x] = dot;
             }
             __syncthreads();
@@ -507,14 +527,54 @@ __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(const Row
     }
 }
 
-// Parts of a row in x (consecutive workgroups share a token), groups of tokens in y; the
-// kernels step over the tokens that a grid does not hold.
-dim3 grid_for(const RowsArgs& a, uint32_t unit)
+constexpr uint64_t kInfinityCache = 256ull << 20;
+
+uint64_t row_bytes(const RowsArgs& a) { return uint64_t(a.row_len) * (a.fp32 ? 4 : 2); }
+
+// Whether tokens and rows together pass what the Infinity Cache holds.
+bool streams(const RowsArgs& a) { return (a.tokens + a.nrows) * row_bytes(a) > kInfinityCache; }
+
+// Rows that stream go by waves where they start at lines and fill nine tenths of their
+// 64-chunk parts (345 us against 365 by lanes for the combine above; fp32 rows of 4098, 67 us
+// by lanes and 82 by waves).  What fits the caches is as fast or faster by lanes (4096 tokens
+// of 4096 to 4 rows each, 25.2 us and 28.7).
+bool goes_by_waves(const RowsArgs& a)
 {
-    const uint64_t bytes = uint64_t(a.row_len) * (a.fp32 ? 4 : 2);
-    const uint64_t parts = ((bytes + unit - 1) / unit + 63) / 64;
-    const uint64_t groups = (a.tokens + kRowWaves - 1) / kRowWaves;
+    const uint64_t chunks = (row_bytes(a) + 15) / 16;
+    const uint64_t starts = reinterpret_cast<uintptr_t>(a.src) | reinterpret_cast<uintptr_t>(a.dst) | a.src_stride |
+                            a.dst_stride;
+    return row_bytes(a) >= 16 && streams(a) && starts % 128 == 0 && 10 * chunks >= 9 * ((chunks + 63) / 64 * 64);
+}
+
+dim3 wave_grid(const RowsArgs& a)
+{
+    const uint64_t parts = ((row_bytes(a) + 15) / 16 + 63) / 64, groups = (a.tokens + kRowWaves - 1) / kRowWaves;
     return dim3(uint32_t(parts), uint32_t(groups < 65535 ? groups : 65535));
+}
+
+dim3 lane_grid(RowsArgs& a, uint32_t unit)
+{
+    const uint64_t chunks = (row_bytes(a) + unit - 1) / unit;
+    // slices of at most 2^24 chunks (2^30 bytes of threads' indices stay far below 2^31)
+    const uint64_t most = (1ull << 24) / chunks > 0 ? (1ull << 24) / chunks : 1;
+    a.slice = uint32_t(a.tokens < most ? a.tokens : most);
+    a.shift = 31;
+    while ((1ull << (a.shift - 31)) < chunks) a.shift++;
+    a.inverse = uint32_t(((1ull << a.shift) + chunks - 1) / chunks);
+    const uint64_t blocks = (a.slice * chunks + kRowThreads - 1) / kRowThreads;
+    const uint64_t slices = (a.tokens + a.slice - 1) / a.slice;
+    return dim3(uint32_t((blocks + 7) / 8 * 8), uint32_t(slices < 65535 ? slices : 65535));
+}
+
+// Lanes per token of the combine's gradient: a workgroup above 2 KB a row (4 KB, 10000
+// tokens of 4 choices: 61.5 us, 70.3 with a wave each), or where there are few tokens (64 of
+// 8 choices at 2 KB: 6.0 and 7.9); else the part of a wave that takes a row at once (11
+// chunks: 9.2 us on 16 lanes, 12.8 on 32; 38 chunks: 23.4 on 64, 24.2 on 32).
+uint32_t backward_lanes(const RowsArgs& a, uint32_t unit)
+{
+    const uint64_t chunks = (row_bytes(a) + unit - 1) / unit;
+    if (unit == 16 && (row_bytes(a) > 2048 || a.tokens < 1024)) return kRowThreads;
+    return chunks <= 8 ? 8 : chunks <= 16 ? 16 : chunks <= 32 ? 32 : 64;
 }
 
 }  // namespace
@@ -543,42 +603,73 @@ hipError_t launch_moe_sort(const SortArgs& a, hipStream_t s)
     }
 }
 
-hipError_t launch_moe_dispatch(const RowsArgs& a, hipStream_t s)
+hipError_t launch_moe_dispatch(const RowsArgs& args, hipStream_t s)
 {
-    const dim3 block(kRowThreads);
-    if (a.row_len * (a.fp32 ? 4ull : 2ull) >= 16) hipLaunchKernelGGL(dispatch_kernel<16>, grid_for(a, 16), block, 0, s, a);
-    else if (a.fp32) hipLaunchKernelGGL(dispatch_kernel<4>, grid_for(a, 4), block, 0, s, a);
-    else hipLaunchKernelGGL(dispatch_kernel<2>, grid_for(a, 2), block, 0, s, a);
+    RowsArgs a = args;
+    const auto run = [&](auto kernel, dim3 grid) { hipLaunchKernelGGL(kernel, grid, dim3(kRowThreads), 0, s, a); };
+    if (goes_by_waves(a)) run(dispatch_kernel<true, 16, true>, wave_grid(a));
+    else if (row_bytes(a) < 16 && a.fp32) run(dispatch_kernel<false, 4, false>, lane_grid(a, 4));
+    else if (row_bytes(a) < 16) run(dispatch_kernel<false, 2, false>, lane_grid(a, 2));
+    else if (streams(a)) run(dispatch_kernel<false, 16, true>, lane_grid(a, 16));
+    else run(dispatch_kernel<false, 16, false>, lane_grid(a, 16));
     return hipGetLastError();
 }
 
-hipError_t launch_moe_combine(const RowsArgs& a, hipStream_t s)
+hipError_t launch_moe_combine(const RowsArgs& args, hipStream_t s)
 {
-    const dim3 block(kRowThreads);
-    if (a.row_len * (a.fp32 ? 4ull : 2ull) >= 16) {
-        if (a.fp32) hipLaunchKernelGGL((combine_kernel<true, 16>), grid_for(a, 16), block, 0, s, a);
-        else hipLaunchKernelGGL((combine_kernel<false, 16>), grid_for(a, 16), block, 0, s, a);
-    } else if (a.fp32) {
-        hipLaunchKernelGGL((combine_kernel<true, 4>), grid_for(a, 4), block, 0, s, a);
+    RowsArgs a = args;
+    const auto run = [&](auto kernel, dim3 grid) { hipLaunchKernelGGL(kernel, grid, dim3(kRowThreads), 0, s, a); };
+    if (row_bytes(a) < 16) {
+        if (a.fp32) run(combine_kernel<false, true, 4, false>, lane_grid(a, 4));
+        else run(combine_kernel<false, false, 2, false>, lane_grid(a, 2));
+    } else if (goes_by_waves(a)) {
+        if (a.fp32) run(combine_kernel<true, true, 16, true>, wave_grid(a));
+        else run(combine_kernel<true, false, 16, true>, wave_grid(a));
+    } else if (streams(a)) {
+        if (a.fp32) run(combine_kernel<false, true, 16, true>, lane_grid(a, 16));
+        else run(combine_kernel<false, false, 16, true>, lane_grid(a, 16));
     } else {
-        hipLaunchKernelGGL((combine_kernel<false, 2>), grid_for(a, 2), block, 0, s, a);
+        if (a.fp32) run(combine_kernel<false, true, 16, false>, lane_grid(a, 16));
+        else run(combine_kernel<false, false, 16, false>, lane_grid(a, 16));
     }
     return hipGetLastError();
 }
 
-hipError_t launch_moe_combine_backward(const RowsArgs& a, hipStream_t s)
+namespace {
+
+template <bool FP32, uint32_t BYTES, bool kStream>
+void run_backward(const RowsArgs& a, hipStream_t s)
 {
-    const uint64_t bytes = a.row_len * (a.fp32 ? 4ull : 2ull);
-    const auto run = [&](auto kernel, uint32_t tokens) {   // tokens of a workgroup
-        const uint64_t groups = (a.tokens + tokens - 1) / tokens;
+    const uint32_t lanes = backward_lanes(a, BYTES);
+    const auto run = [&](auto kernel) {
+        const uint64_t per = kRowThreads / lanes, groups = (a.tokens + per - 1) / per;
         hipLaunchKernelGGL(kernel, dim3(uint32_t(groups < (1u << 20) ? groups : 1u << 20)), dim3(kRowThreads), 0, s, a);
     };
-    // a wave per token up to 2 KB a row (8192 tokens of 4 choices: 28 us against 31 with a
-    // workgroup each at 2 KB, 60 and 53 at 4 KB), with enough tokens to fill the GPU (64 of
-    // 8 choices, 2 KB: 7.9 and 6.0)
-    if (bytes < 16) a.fp32 ? run(combine_backward_kernel<true, 4, 1>, 4) : run(combine_backward_kernel<false, 2, 1>, 4);
-    else if (bytes <= 2048 && a.tokens >= 1024) a.fp32 ? run(combine_backward_kernel<true, 16, 1>, 4) : run(combine_backward_kernel<false, 16, 1>, 4);
-    else a.fp32 ? run(combine_backward_kernel<true, 16, 4>, 1) : run(combine_backward_kernel<false, 16, 4>, 1);
+    switch (lanes) {
+        case 8: run(combine_backward_kernel<FP32, BYTES, 8, kStream>); break;
+        case 16: run(combine_backward_kernel<FP32, BYTES, 16, kStream>); break;
+        case 32: run(combine_backward_kernel<FP32, BYTES, 32, kStream>); break;
+        case 64: run(combine_backward_kernel<FP32, BYTES, 64, kStream>); break;
+        default: run(combine_backward_kernel<FP32, BYTES, kRowThreads, kStream>); break;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_moe_combine_backward(const RowsArgs& a, hipStream_t s)
+{
+    // tokens' gradients, rows and their gradients
+    const bool stream = (a.tokens + 2ull * a.nrows) * row_bytes(a) > kInfinityCache;
+    if (row_bytes(a) < 16) {
+        if (a.fp32) run_backward<true, 4, false>(a, s);
+        else run_backward<false, 2, false>(a, s);
+    } else if (stream) {
+        if (a.fp32) run_backward<true, 16, true>(a, s);
+        else run_backward<false, 16, true>(a, s);
+    } else {
+        if (a.fp32) run_backward<true, 16, false>(a, s);
+        else run_backward<false, 16, false>(a, s);
+    }
     return hipGetLastError();
 }
 

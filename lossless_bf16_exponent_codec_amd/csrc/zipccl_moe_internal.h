@@ -50,6 +50,9 @@ struct RowsArgs {
     uint32_t row_len;        // values
     uint32_t top_k;
     uint32_t fp32;           // 1: fp32 values, 0: BF16
+    // filled in by the launches: i / chunks of a row = i * inverse >> shift for i < 2^31, and
+    // the tokens of one slice of the grid
+    uint32_t inverse, shift, slice;
 };
 hipError_t launch_moe_dispatch(const RowsArgs& a, hipStream_t s);
 hipError_t launch_moe_combine(const RowsArgs& a, hipStream_t s);

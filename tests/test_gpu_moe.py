@@ -382,6 +382,45 @@ def test_many_tokens_step_over_the_grid(Z):
     assert torch.equal(out, x)
 
 
+@pytest.mark.parametrize("dtype,T,K,H", [
+    (torch.bfloat16, 2000, 16, 4096), (torch.bfloat16, 2000, 16, 4099), (torch.float32, 1500, 20, 2048),
+    (torch.float32, 1500, 20, 2051), (torch.bfloat16, 40000, 6, 515), (torch.bfloat16, 140000, 1, 1030),
+    (torch.bfloat16, 3000000, 1, 7), (torch.float32, 6000000, 1, 3)])
+def test_more_than_the_caches_and_one_slice(Z, dtype, T, K, H):
+    # rows and tokens past the Infinity Cache, and more chunks than a slice of the grid
+    g = torch.Generator(device="cuda").manual_seed(H)
+    M = T * K - T // 3
+    perm = torch.randperm(T * K, generator=g, device="cuda")
+    s = torch.where(perm < M, perm, -1).int().view(T, K)
+    x = torch.randn(T, H, generator=g, device="cuda").to(dtype)
+    w = torch.rand(T, K, generator=g, device="cuda")
+    flat = s.view(-1)
+    kept = torch.nonzero(flat >= 0).squeeze(1)
+    token, row = kept // K, flat[kept].long()
+    y = poisoned(M, H, dtype)
+    Z.moe_dispatch(x, s, y)
+    assert torch.equal(y[row], x[token])
+    y = torch.randn(M, H, generator=g, device="cuda").to(dtype)
+    for weights, run in ((None, lambda out: Z.moe_dispatch_backward(y, s, out)), (w, lambda out: Z.moe_combine(y, s, w, out))):
+        out = poisoned(T, H, dtype)
+        run(out)
+        for a in range(0, T, 1 << 19):   # in parts: 64-bit copies are large
+            b = min(T, a + (1 << 19))
+            terms = [torch.where((s[a:b, k] >= 0).unsqueeze(1), y[s[a:b, k].clamp(min=0).long()].double(), 0.0)
+                     * (1.0 if weights is None else w[a:b, k:k + 1].double()) for k in range(K)]
+            want, size = sum(terms), sum(t.abs() for t in terms)
+            assert bool(((out[a:b].double() - want).abs() <= rel(dtype) * want.abs() + K * 2.0 ** -23 * size).all())
+    dy, dw = poisoned(M, H, dtype), torch.full((T, K), POISON, device="cuda")
+    Z.moe_combine_backward(x, y, s, w, dy, dw)
+    for a in range(0, kept.numel(), 1 << 17):
+        t, r, at = token[a:a + (1 << 17)], row[a:a + (1 << 17)], kept[a:a + (1 << 17)]
+        want = x[t].double() * w.view(-1)[at].double().unsqueeze(1)
+        assert bool(((dy[r].double() - want).abs() <= (rel(dtype) + 2.0 ** -23) * want.abs() + TINY).all())
+        dots = x[t].double() * y[r].double()
+        assert bool(((dw.view(-1)[at].double() - dots.sum(1)).abs() <= H * 2.0 ** -23 * dots.abs().sum(1)).all())
+    assert not dw.view(-1)[flat < 0].any()
+
+
 # ------------------------------------------------------------------------------------
 # 8-bit rows
 # ------------------------------------------------------------------------------------
