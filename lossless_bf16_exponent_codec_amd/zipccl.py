@@ -552,27 +552,35 @@ def _matrix(t, what, dtype=None):
     """(address, rows, row length, row stride) of a 2-D row-major tensor."""
     if t.dim() != 2:
         raise ValueError(f"{what} is a 2-D tensor")
-    (rows, length), (stride, step) = t.shape, t.stride()
-    if step != 1 and length > 1 and rows > 0:
-        raise ValueError(f"{what} has contiguous rows")
-    if stride < length and rows > 1:
-        raise ValueError(f"{what} has rows that do not overlap")
-    if t.dtype not in _DTYPES if dtype is None else t.dtype is not dtype:
+    rows, length = t.shape
+    if t.is_contiguous():
+        stride = length
+    else:
+        stride, step = t.stride()
+        if rows > 0 and length > 1 and step != 1:
+            raise ValueError(f"{what} has contiguous rows")
+        if rows > 1 and stride < length:
+            raise ValueError(f"{what} has rows that do not overlap")
+        stride = max(stride, length)
+    if t.dtype is not dtype and (dtype is not None or t.dtype not in _DTYPES):
         raise ValueError(f"{what} is {t.dtype}")
-    return t.data_ptr(), rows, length, stride if stride > length else length
+    return t.data_ptr(), rows, length, stride
 
 
 def _vector(t, n, dtype, what):
     """Address of a contiguous tensor of at least n values."""
-    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
-        raise ValueError(f"{what} is a contiguous {dtype} tensor of at least {n} values")
-    return t.data_ptr()
+    if t.dtype is dtype and t.is_contiguous() and t.numel() >= n:
+        return t.data_ptr()
+    raise ValueError(f"{what} is a contiguous {dtype} tensor of at least {n} values")
 
 
 def _slots(slots, tokens):
-    if slots.dim() != 2 or slots.shape[0] != tokens:
-        raise ValueError(f"slots is tokens x top_k, {tokens} tokens")
-    return _vector(slots, 0, torch.int32, "slots"), slots.shape[1]
+    """(address, top_k) of tokens x top_k slots."""
+    if slots.dim() == 2 and slots.dtype is torch.int32 and slots.is_contiguous():
+        rows, top_k = slots.shape
+        if rows == tokens:
+            return slots.data_ptr(), top_k
+    raise ValueError(f"slots is a contiguous int32 tensor, tokens x top_k, of {tokens} tokens")
 
 
 def _same(a, b, what):
