@@ -7,14 +7,14 @@
 // a call gives the same bits on every run.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "zipccl.h"
 #include "zipccl_moe_internal.h"
 
 namespace zc {
 
 namespace {
-
-template <uint32_t N> struct Constant { static constexpr uint32_t value = N; };
 
 __device__ inline uint32_t lane_id() { return __lane_id(); }
 
@@ -36,9 +36,9 @@ __device__ inline void set_status(uint32_t* status, uint32_t bits)
 // Nothing here is bound by bandwidth (2 MB for 131072 choices); what counts is the chain
 // of dependent steps.  A wave therefore ranks its choices once, holds the ranks in
 // registers across the scan over experts, and adds the expert's base after it.  Over 256
-// experts 512 choices take 3.4 us (one launch, near the shortest one), 131072 take 9.8:
-// 2.9 to count, the rest to place, which reads the other workgroups' counts (16 loads in
-// flight per thread; one after another they took 3 us more).
+// experts 512 choices take 3.4 us (one launch, near the shortest one), 131072 take 9.0:
+// 2.9 to count, the rest to place, which reads the other workgroups' counts (8 16-byte loads
+// in flight per thread; 16 of 4 bytes took 0.8 us more, one after another 3 more still).
 // ------------------------------------------------------------------------------------
 __device__ inline int32_t load_id(const SortArgs& a, uint32_t i, bool& bad)
 {
@@ -58,6 +58,9 @@ __device__ inline uint32_t sort_block(const SortArgs& a)
     return a.blocks > 1 ? blockIdx.x % 8 * ((a.blocks + 7) / 8) + blockIdx.x / 8 : 0;
 }
 
+// Counts of a block in the workspace: the experts, padded to whole 16 bytes.
+__host__ __device__ inline uint32_t count_row(const SortArgs& a) { return (a.experts + 3) & ~3u; }
+
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const SortArgs a)
 {
     const uint32_t block = sort_block(a);
@@ -72,9 +75,12 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const SortArgs
         if (id >= 0) atomicAdd(&s_count[id], 1u);
     }
     __syncthreads();
-    for (uint32_t e = threadIdx.x; e < a.experts; e += kSortThreads)
-        a.hist[uint64_t(block) * a.experts + e] = s_count[e];
+    const uint32_t wide = count_row(a);
+    for (uint32_t e = threadIdx.x; e < wide; e += kSortThreads)
+        a.hist[uint64_t(block) * wide + e] = e < a.experts ? s_count[e] : 0;
 }
+
+constexpr uint32_t kMostShares = 16;   // of the other workgroups' counts, summed by one thread
 
 // kGroups: groups of 64 choices per wave held in registers; 0: any number, ranked twice.
 template <uint32_t kGroups>
@@ -82,9 +88,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const SortArgs
 {
     const uint32_t block = sort_block(a);
     if (block >= a.blocks) return;
-    extern __shared__ uint32_t s_next[];            // [wave][expert]: choices so far, then the expert's base
+    extern __shared__ __attribute__((aligned(16))) uint32_t s_next[];            // [wave][expert]: choices so far, then the expert's base
     __shared__ uint32_t s_wave_sum[kSortWaves];
-    __shared__ uint32_t s_before[kSortThreads], s_all[kSortThreads];
     const uint32_t tid = threadIdx.x, lane = lane_id();
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t E = a.experts;
@@ -101,30 +106,49 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const SortArgs
             id[g] = i < end ? load_id(a, i, bad) : -1;
         }
     }
-    // the other workgroups' counts: threads share an expert's blocks where there are
-    // more threads than experts
+    // The other workgroups' counts.  A thread takes four experts and every `shares`-th
+    // block; the shares meet in LDS, where thread e picks up expert e: its choices in the
+    // blocks before this one, and in all.
+    uint32_t before = 0, all = 0;
     if (a.blocks > 1) {
-        const uint32_t shares = kSortThreads / E, e = tid % E, share = tid / E;
-        uint32_t before = 0, all = 0;
+        const uint32_t wide = count_row(a), fours = wide / 4, shares = min(kSortThreads / fours, kMostShares);
+        const uint32_t four = tid % fours, share = tid / fours;
+        uint4 b4 = make_uint4(0, 0, 0, 0), a4 = make_uint4(0, 0, 0, 0);
         const auto gather = [&](auto batch) {   // loads in flight
             constexpr uint32_t kBatch = decltype(batch)::value;
             for (uint32_t b0 = 0; b0 < a.blocks; b0 += kBatch * shares) {
-                uint32_t c[kBatch];
+                uint4 c[kBatch];
 #pragma unroll
-                for (uint32_t j = 0; j < kBatch; j++) c[j] = a.hist[min(b0 + j * shares + share, a.blocks - 1) * E + e];
+                for (uint32_t j = 0; j < kBatch; j++) {
+                    const uint32_t b = min(b0 + j * shares + share, a.blocks - 1);
+                    c[j] = *reinterpret_cast<const uint4*>(a.hist + uint64_t(b) * wide + 4 * four);
+                }
 #pragma unroll
                 for (uint32_t j = 0; j < kBatch; j++) {
                     const uint32_t b = b0 + j * shares + share;
-                    all += b < a.blocks ? c[j] : 0;
-                    before += b < block ? c[j] : 0;
+                    if (b < a.blocks) a4 = make_uint4(a4.x + c[j].x, a4.y + c[j].y, a4.z + c[j].z, a4.w + c[j].w);
+                    if (b < block) b4 = make_uint4(b4.x + c[j].x, b4.y + c[j].y, b4.z + c[j].z, b4.w + c[j].w);
                 }
             }
         };
-        if (a.blocks > 4 * shares) gather(Constant<16>());
-        else gather(Constant<4>());
-        if (share >= shares) before = all = 0;   // threads past the last whole share
-        s_before[tid] = before;
-        s_all[tid] = all;
+        if (share < shares) {
+            if (a.blocks > shares) gather(std::integral_constant<uint32_t, 8>());
+            else gather(std::integral_constant<uint32_t, 1>());
+        }
+        uint32_t* sums = s_next;   // [share][wide] before, then the same of all
+        if (share < shares) {
+            *reinterpret_cast<uint4*>(sums + share * wide + 4 * four) = b4;
+            *reinterpret_cast<uint4*>(sums + (shares + share) * wide + 4 * four) = a4;
+        }
+        __syncthreads();
+        if (tid < E) {
+#pragma unroll 8
+            for (uint32_t v = 0; v < shares; v++) {
+                before += sums[v * wide + tid];
+                all += sums[(shares + v) * wide + tid];
+            }
+        }
+        __syncthreads();
     }
     for (uint32_t j = tid; j < kSortWaves * E; j += kSortThreads) s_next[j] = 0;
     __syncthreads();
@@ -161,18 +185,10 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const SortArgs
     if (bad) set_status(a.status, ZIPCCL_STATUS_BAD_INDEX);
     __syncthreads();
 
-    // thread e: the expert's choices in this block, in the blocks before it, and in all
-    uint32_t before = 0, all = 0;
-    if (tid < E) {
-        if (a.blocks > 1) {
-            for (uint32_t share = 0; share < kSortThreads / E; share++) {
-                before += s_before[share * E + tid];
-                all += s_all[share * E + tid];
-            }
-        } else {
+    // one block: thread e's choices in all are those of the waves
+    if (a.blocks == 1 && tid < E) {
 #pragma unroll
-            for (uint32_t w = 0; w < kSortWaves; w++) all += s_next[w * E + tid];
-        }
+        for (uint32_t w = 0; w < kSortWaves; w++) all += s_next[w * E + tid];
     }
     // exclusive sum of `all` over the experts
     uint32_t scan = all;
@@ -587,8 +603,10 @@ hipError_t launch_moe_sort(const SortArgs& a, hipStream_t s)
     const dim3 grid(a.blocks > 1 ? (a.blocks + 7) / 8 * 8 : 1), block(kSortThreads);
     if (a.blocks > 1) hipLaunchKernelGGL(sort_count_kernel, grid, block, 0, s, a);
     const auto place = [&](void (*kernel)(SortArgs)) -> hipError_t {
-        const uint32_t lds = kSortWaves * a.experts * 4;
-        if (lds > 32768) {   // with the kernel's own arrays more than the 64 KB a launch has by default
+        // the waves' counters; before them the shares' sums, twice
+        uint32_t lds = kSortWaves * a.experts * 4;
+        if (a.blocks > 1 && lds < 2 * kSortThreads * 16) lds = 2 * kSortThreads * 16;
+        if (lds > 61440) {   // with the kernel's own few bytes close to the 64 KB a launch has by default
             if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                                    hipFuncAttributeMaxDynamicSharedMemorySize, int(lds)))
                 return e;

@@ -51,9 +51,9 @@ zipccl_status check_slots(const int32_t* slots, uint64_t tokens, int top_k, uint
 
 // n choices split over the sort's workgroups, in groups of 64 per wave: one workgroup (one
 // launch) up to 2048 choices (5.1 us at 2048 over 256 experts, 6.7 as two launches; at 4096
-// 7.6 and 6.8), else the fewest groups that leave at most 128 workgroups (131072 choices:
-// 9.8 us at 64 or 128 workgroups, 12.6 at 32; 524288: 12.7 at 128, 17 at 64, 26 at 32),
-// and past 16 groups as many workgroups as the workspace has counts for.
+// 7.6 and 7.2), else the fewest groups that leave at most 128 workgroups (131072 choices
+// over 256 experts: 9.0 us, as at 64 workgroups, 12.6 at 32; 524288 over 64: 12.2 at 128, 17
+// at 64, 26 at 32), and past 16 groups as many workgroups as the workspace has counts for.
 void split_choices(SortArgs& a)
 {
     constexpr uint32_t kOneBlock = 2 * kSortThreads, kBlocks = 128;
