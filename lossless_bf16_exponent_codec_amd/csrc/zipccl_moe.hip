@@ -256,8 +256,8 @@ template <> struct Raw<4> { typedef uint32_t type; };
 template <> struct Raw<2> { typedef uint16_t type; };
 
 // kStream: non-temporal accesses, for rows that do not fit the Infinity Cache (16384 tokens
-// of 7168 to 8 rows each, 1.9 GB: dispatch 343 us, 385 with plain stores; combine 345 us,
-// 400 with plain loads).  What fits is left to the caches (4096 tokens of 4098 to 4 rows
+// of 7168 to 8 rows each, 1.9 GB: dispatch 346 us, 385 with plain stores; combine 345 us,
+// 400 with plain loads, the tokens in the cache).  What fits is left to the caches (4096 tokens of 4098 to 4 rows
 // each, 168 MB: dispatch 26.4 us, 36.4 with non-temporal stores, whose lines at the ends of
 // rows are written in parts; combine 25.1 and 30.6).
 typedef uint32_t Quad __attribute__((ext_vector_type(4), aligned(2)));
@@ -423,8 +423,7 @@ __device__ inline void combine_chunk(const RowsArgs& a, uint64_t token, uint32_t
 //
 // By waves: a wave takes 64 consecutive chunks (1 KB) of one token, whose slots and
 // weights are then scalar values.  Parts of a row in x, so that consecutive workgroups
-// share a token, groups of tokens in y.  For rows that fill such parts (2 and 4 KB per
-// wave were slower: 350 and 369 us for the dispatch above).
+// share a token, groups of tokens in y.  For rows that fill such parts.
 template <class Take>
 __device__ inline void by_waves(const RowsArgs& a, const RowShape& sh, Take&& take)
 {
@@ -451,13 +450,38 @@ __device__ inline void by_lanes(const RowsArgs& a, const RowShape& sh, Take&& ta
         take(token, sh.at<BYTES>(i - in * sh.chunks));
 }
 
-template <bool kWaves, uint32_t BYTES, bool kStream>
+template <uint32_t BYTES, bool kStream>
 __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(const RowsArgs a)
 {
     const RowShape sh = shape_of<BYTES>(a);
-    const auto take = [&](uint64_t token, uint32_t at) { dispatch_chunk<BYTES, kStream>(a, token, at); };
-    if constexpr (kWaves) by_waves(a, sh, take);
-    else by_lanes<BYTES>(a, sh, take);
+    by_lanes<BYTES>(a, sh, [&](uint64_t token, uint32_t at) { dispatch_chunk<BYTES, kStream>(a, token, at); });
+}
+
+// Dispatch by waves, for rows that stream: kShare waves load the same 1 KB of a token (one
+// of them from memory) and write it to every kShare-th of its slots, kParts neighbouring KB
+// per workgroup.  16384 tokens of 7168 from HBM to 8 rows each: 351 us, 417 where one wave
+// wrote all 8 rows (4 waves, 1 KB per workgroup 368; 2 waves, 2 KB 374; 1 wave, 4 KB 384).
+// Two rows per wave are best: at 4 rows 2 waves take 203 us, 4 take 243, 1 takes 217.
+constexpr uint32_t kParts = 4;
+
+template <uint32_t kShare>
+__global__ __launch_bounds__(64 * kShare * kParts) void dispatch_shared_kernel(const RowsArgs a)
+{
+    const RowShape sh = shape_of<16>(a);
+    const uint32_t parts = (sh.chunks + 63) / 64;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t item = blockIdx.x * kParts + wave / kShare, in = item / parts;
+    const uint32_t c = (item - in * parts) * 64 + lane_id();
+    if (in >= a.slice || c >= sh.chunks) return;
+    const uint32_t at = sh.at<16>(c);
+    for (uint64_t token = uint64_t(blockIdx.y) * a.slice + in; token < a.tokens; token += uint64_t(gridDim.y) * a.slice) {
+        const auto v = load_raw<16, false>(a.src + token * a.src_stride + at);
+        for (uint32_t k = wave % kShare; k < a.top_k; k += kShare) {
+            const int32_t s = a.slots[token * a.top_k + k];
+            if (s >= int32_t(a.nrows)) set_status(a.status, ZIPCCL_STATUS_BAD_INDEX);
+            else if (s >= 0) store_raw<16, true>(a.dst + uint64_t(uint32_t(s)) * a.dst_stride + at, v);
+        }
+    }
 }
 
 template <bool kWaves, bool FP32, uint32_t BYTES, bool kStream>
@@ -553,7 +577,7 @@ uint64_t row_bytes(const RowsArgs& a) { return uint64_t(a.row_len) * (a.fp32 ? 4
 // Whether tokens and rows together pass what the Infinity Cache holds.
 bool streams(const RowsArgs& a) { return (a.tokens + a.nrows) * row_bytes(a) > kInfinityCache; }
 
-// Rows that stream go by waves where they start at lines and fill nine tenths of their
+// Rows that stream go by waves (combine) or by shared waves (dispatch) where they start at lines and fill nine tenths of their
 // 64-chunk parts (345 us against 365 by lanes for the combine above; fp32 rows of 4098, 67 us
 // by lanes and 82 by waves).  What fits the caches is as fast or faster by lanes (4096 tokens
 // of 4096 to 4 rows each, 25.2 us and 28.7).
@@ -569,6 +593,15 @@ dim3 wave_grid(const RowsArgs& a)
 {
     const uint64_t parts = ((row_bytes(a) + 15) / 16 + 63) / 64, groups = (a.tokens + kRowWaves - 1) / kRowWaves;
     return dim3(uint32_t(parts), uint32_t(groups < 65535 ? groups : 65535));
+}
+
+dim3 shared_grid(RowsArgs& a)
+{
+    const uint64_t parts = ((row_bytes(a) + 15) / 16 + 63) / 64;
+    const uint64_t most = (1ull << 22) / parts > 0 ? (1ull << 22) / parts : 1;   // tokens of a slice
+    a.slice = uint32_t(a.tokens < most ? a.tokens : most);
+    const uint64_t slices = (a.tokens + a.slice - 1) / a.slice;
+    return dim3(uint32_t((a.slice * parts + kParts - 1) / kParts), uint32_t(slices < 65535 ? slices : 65535));
 }
 
 dim3 lane_grid(RowsArgs& a, uint32_t unit)
@@ -627,12 +660,21 @@ hipError_t launch_moe_sort(const SortArgs& a, hipStream_t s)
 hipError_t launch_moe_dispatch(const RowsArgs& args, hipStream_t s)
 {
     RowsArgs a = args;
-    const auto run = [&](auto kernel, dim3 grid) { hipLaunchKernelGGL(kernel, grid, dim3(kRowThreads), 0, s, a); };
-    if (goes_by_waves(a)) run(dispatch_kernel<true, 16, true>, wave_grid(a));
-    else if (row_bytes(a) < 16 && a.fp32) run(dispatch_kernel<false, 4, false>, lane_grid(a, 4));
-    else if (row_bytes(a) < 16) run(dispatch_kernel<false, 2, false>, lane_grid(a, 2));
-    else if (streams(a)) run(dispatch_kernel<false, 16, true>, lane_grid(a, 16));
-    else run(dispatch_kernel<false, 16, false>, lane_grid(a, 16));
+    const auto run = [&](auto kernel, dim3 grid, uint32_t threads = kRowThreads) {
+        hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, s, a);
+    };
+    if (goes_by_waves(a)) {
+        if (a.top_k >= 7) run(dispatch_shared_kernel<4>, shared_grid(a), 256 * kParts);
+        else if (a.top_k >= 2) run(dispatch_shared_kernel<2>, shared_grid(a), 128 * kParts);
+        else run(dispatch_shared_kernel<1>, shared_grid(a), 64 * kParts);
+    } else if (row_bytes(a) < 16) {
+        if (a.fp32) run(dispatch_kernel<4, false>, lane_grid(a, 4));
+        else run(dispatch_kernel<2, false>, lane_grid(a, 2));
+    } else if (streams(a)) {
+        run(dispatch_kernel<16, true>, lane_grid(a, 16));
+    } else {
+        run(dispatch_kernel<16, false>, lane_grid(a, 16));
+    }
     return hipGetLastError();
 }
 

@@ -383,7 +383,8 @@ def test_many_tokens_step_over_the_grid(Z):
 
 
 @pytest.mark.parametrize("dtype,T,K,H", [
-    (torch.bfloat16, 2000, 16, 4096), (torch.bfloat16, 2000, 16, 4099), (torch.float32, 1500, 20, 2048),
+    (torch.bfloat16, 2000, 16, 4096), (torch.bfloat16, 9000, 3, 4096), (torch.bfloat16, 9000, 1, 16320),
+    (torch.bfloat16, 2000, 16, 4099), (torch.float32, 1500, 20, 2048),
     (torch.float32, 1500, 20, 2051), (torch.bfloat16, 40000, 6, 515), (torch.bfloat16, 140000, 1, 1030),
     (torch.bfloat16, 3000000, 1, 7), (torch.float32, 6000000, 1, 3)])
 def test_more_than_the_caches_and_one_slice(Z, dtype, T, K, H):
@@ -419,6 +420,21 @@ def test_more_than_the_caches_and_one_slice(Z, dtype, T, K, H):
         dots = x[t].double() * y[r].double()
         assert bool(((dw.view(-1)[at].double() - dots.sum(1)).abs() <= H * 2.0 ** -23 * dots.abs().sum(1)).all())
     assert not dw.view(-1)[flat < 0].any()
+
+
+def test_dispatch_of_more_than_one_slice_of_streamed_rows(Z):
+    T, H = 540000, 4096   # 8 KB a row: 2^22 parts are 524288 tokens
+    x = torch.randint(-30000, 30000, (T, H), dtype=torch.int16, device="cuda").view(torch.bfloat16)
+    s = torch.randperm(T, device="cuda").int().view(T, 1)
+    s[7] = -1
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = torch.zeros_like(x)
+    Z.moe_dispatch(x, s, y, status)
+    kept = torch.nonzero(s.view(-1) >= 0).squeeze(1)
+    assert int(status.item()) == 0 and torch.equal(y[s.view(-1)[kept].long()].view(torch.int16), x[kept].view(torch.int16))
+    s[9] = T
+    Z.moe_dispatch(x, s, y, status)
+    assert int(status.item()) == Z.STATUS_BAD_INDEX
 
 
 # ------------------------------------------------------------------------------------
