@@ -111,9 +111,11 @@ def test_sort_out_of_range_ids_are_dropped_and_reported(Z, T):
     assert np.array_equal(rows.cpu().numpy(), wrows)
 
 
-def test_sort_large(Z):
-    # 2^21 choices, past the workspace's block limit; against a stable sort
-    T, K, E = 1 << 18, 8, 256
+@pytest.mark.parametrize("T,E", [(1 << 18, 256), (300001, 1000), (700003, 77)])
+def test_sort_large(Z, T, E):
+    # 2^21 choices and more, the last past 256 workgroups of 16 groups per wave; against a
+    # stable sort
+    K = 8
     g = torch.Generator(device="cuda").manual_seed(3)
     ids = torch.randint(-3, E, (T, K), generator=g, device="cuda")
     off = torch.empty(E + 1, dtype=torch.int32, device="cuda")
@@ -553,6 +555,7 @@ def test_product(Z, counts, N, H, dtype):
     ([8400], 2048, 256),                  # a round of 256 and 8 tiles over
     ([5000, 3000, 300, 77], 2050, 384),   # 35 x 9, 59 over; edges inside tiles on both sides
     ([100] * 3 + [40000], 513, 130),      # most rows with one expert
+    ([300] * 70, 1024, 128),              # more experts than lanes
     ([130] * 64, 300, 200), ([40] * 100, 200, 300), ([64] * 20, 2000, 128)])
 def test_product_many_tiles(Z, counts, N, H):
     check_product(Z, np.random.default_rng(N), counts, N, H, torch.bfloat16)
