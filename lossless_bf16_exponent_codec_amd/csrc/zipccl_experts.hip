@@ -751,7 +751,11 @@ uint64_t split_workgroups(const ProductArgs& a) { return most_tiles(a, 64) * col
 //    Many: 64 x 128, which read the rows half as often (256 choices over 32 skewed
 //    experts, 2048 x 7168: 78 against 94 at 64 x 64; 1024 over 128: 279 and 286);
 //  - 256 x 256 from 192 rows on when there is a round of it (8 experts, 2048 rows each,
-//    2048 x 7168: 212 against 246 at 128 x 128; 512 rows each, half a round: 78 and 62);
+//    2048 x 7168: 212 against 246 at 128 x 128; 512 rows each, half a round: 78 and 62), rows
+//    are long enough to make up for one workgroup per CU, which starts and ends alone (1
+//    expert, 16384 rows, 2048 outputs: 37.9 against 29.5 at row_len 256, 80.7 and 82.0 at
+//    2048, 111 and 120 at 3328), and the last column is not mostly empty (8 experts, 4096
+//    rows each, 600 x 4096: 106 and 92);
 //  - else 128 x 128 (32 experts, 128 rows each, 2048 x 7168: 105, 148 at 64 x 64), or 64 x
 //    128 where those would leave too many CUs idle (1 expert, 512 rows, 4096 x 2048, 128
 //    tiles: 12.3 and 10.0; 700 rows, 192 tiles: 12.8 and 14.3).
@@ -766,7 +770,8 @@ Shape choose(const ProductArgs& a)
         const uint64_t n = tiles(64, 64);
         return n <= kCus + kCus / 2 ? Shape::narrow_deep : n <= 3 * kCus ? Shape::narrow : Shape::wide;
     }
-    if (each >= 192 && tiles(256, 256) >= kCus) return Shape::large;
+    const bool fits = 9 * 2 * columns(a, 256) <= 10 * columns(a, 128);   // outputs left empty at 256, and at 128
+    if (each >= 192 && a.slabs >= 16 && fits && tiles(256, 256) >= kCus) return Shape::large;
     return tiles(128, 128) <= kCus * 5 / 8 ? Shape::wide : Shape::square;
 }
 

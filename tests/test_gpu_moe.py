@@ -551,11 +551,12 @@ def test_product(Z, counts, N, H, dtype):
 
 
 @pytest.mark.parametrize("counts,N,H", [
-    ([16640], 1280, 128),                 # 65 x 5 tiles of 256 x 256: a part round of 69, a total that is no multiple of 8
-    ([8400], 2048, 256),                  # a round of 256 and 8 tiles over
-    ([5000, 3000, 300, 77], 2050, 384),   # 35 x 9, 59 over; edges inside tiles on both sides
+    ([16640], 1280, 2000),                # 65 x 5 tiles of 256 x 256: a part round of 69, a total that is no multiple of 8
+    ([8400], 2048, 2048),                 # a round of 256 and 8 tiles over
+    ([5000, 3000, 300, 77], 2290, 2100),  # 35 x 9, 59 over; edges inside tiles on both sides
     ([100] * 3 + [40000], 513, 130),      # most rows with one expert
-    ([300] * 70, 1024, 128),              # more experts than lanes
+    ([300] * 70, 1024, 1930),             # more experts than lanes
+    ([16640], 1280, 128), ([8400], 2048, 256), ([5000, 3000, 300, 77], 2050, 384),
     ([130] * 64, 300, 200), ([40] * 100, 200, 300), ([64] * 20, 2000, 128)])
 def test_product_many_tiles(Z, counts, N, H):
     check_product(Z, np.random.default_rng(N), counts, N, H, torch.bfloat16)
