@@ -77,7 +77,8 @@ typedef enum zipccl_status {
 /* Bits OR-ed into the optional device status word. */
 #define ZIPCCL_STATUS_ESC_OVERFLOW 1u  /* escapes did not fit esc_cap; those past it were dropped */
 #define ZIPCCL_STATUS_CORRUPT 2u       /* decode: header or offset table inconsistent; not decoded */
-#define ZIPCCL_STATUS_BAD_INDEX 4u     /* gathered compress: a row index outside the matrix (row 0 was read) */
+#define ZIPCCL_STATUS_BAD_INDEX 4u     /* gathered compress: a row index outside the matrix (row 0 was read);
+                                          mixture-of-experts rows: an expert, slot or offset out of range */
 #define ZIPCCL_STATUS_WAIT_LIMIT 8u    /* compress: a placing workgroup gave up waiting for an encoder's
                                           count (bounded wait); that unit's escapes, offsets and headers
                                           were not written */
@@ -483,7 +484,8 @@ zipccl_status zipccl_quantize_rows(const void* x, uint64_t x_stride, uint64_t to
  *   w             device, num_experts * outputs rows of w_stride bytes in the same layout
  *   w_scales      device fp32[num_experts * outputs]
  *   offsets       device int32[num_experts + 1], ascending, as zipccl_moe_sort writes them;
- *                 values outside 0..rows are clamped; NULL with num_experts == 1: all rows.
+ *                 values outside 0..rows are clamped, and they and descending ones set
+ *                 ZIPCCL_STATUS_BAD_INDEX; NULL with num_experts == 1: all rows.
  *                 Rows outside every expert's range are left as they were.
  * Strides of q and w are multiples of ZIPCCL_ROW_PAD, at most 2^24; q and w are 16-byte
  * aligned.

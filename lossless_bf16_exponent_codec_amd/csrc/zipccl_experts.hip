@@ -206,6 +206,7 @@ __device__ inline void expert_rows(const ProductArgs& a, uint32_t e, uint32_t& b
         return;
     }
     const int64_t lo = a.offsets[e], hi = a.offsets[e + 1];
+    if (lo < 0 || hi < lo || hi > int64_t(a.rows)) set_status(a.status, ZIPCCL_STATUS_BAD_INDEX);
     begin = uint32_t(min(max(lo, int64_t(0)), int64_t(a.rows)));
     end = uint32_t(min(max(hi, int64_t(begin)), int64_t(a.rows)));
 }

@@ -532,7 +532,9 @@ def check_product(Z, rng, counts, N, H, dtype, gap=0):
     q, s, w, ws = product_inputs(rng, M, E, N, H)
     dq, dsc, dw, dws = (torch.from_numpy(v).cuda() for v in (q, s, w, ws))
     out = poisoned(M, N, dtype)
-    Z.experts_product(dq, dsc, dw, dws, H, out, offsets=torch.from_numpy(offsets.astype(np.int32)).cuda())
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    Z.experts_product(dq, dsc, dw, dws, H, out, offsets=torch.from_numpy(offsets.astype(np.int32)).cuda(), status=status)
+    assert int(status.item()) == 0
     want = R.product(q, s, w, ws, offsets)
     got = host(out)
     filled = int(offsets[-1])
@@ -598,8 +600,9 @@ def test_product_offsets_out_of_range_are_clamped(Z):
     dev = [torch.from_numpy(v).cuda() for v in (q, s, w, ws)]
     for offsets in ([-5, 10, 20, 30, 1000], [0, 60, 70, 80, 90], [40, 30, 20, 10, 0], [-9, -8, -7, -6, -5]):
         out = poisoned(M, N, torch.float32)
-        Z.experts_product(*dev, H, out, offsets=torch.tensor(offsets, dtype=torch.int32, device="cuda"))
-        torch.cuda.synchronize()
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        Z.experts_product(*dev, H, out, offsets=torch.tensor(offsets, dtype=torch.int32, device="cuda"), status=status)
+        assert int(status.item()) == Z.STATUS_BAD_INDEX
         clean = [min(max(o, 0), M) for o in offsets]
         if all(a <= b for a, b in zip(clean, clean[1:])):
             want = R.product(q, s, w, ws, clean)
