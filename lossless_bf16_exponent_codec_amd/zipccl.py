@@ -567,6 +567,20 @@ def _matrix(t, what, dtype=None):
     return t.data_ptr(), rows, length, stride
 
 
+def _holds_padding(t, stride, row_len, what, written):
+    """Refuses 8-bit rows whose values from row_len up to the next multiple of ROW_PAD, which
+    the kernels touch, are not the rows' own.  They are where the view's rows hold them; else
+    they lie past the view's columns: inside the tensor's memory, and, where they are written,
+    in the 128 bytes that the row's end began (rows that start at a multiple of ROW_PAD)."""
+    rows, wide = t.shape
+    padded = -(-row_len // ROW_PAD) * ROW_PAD
+    if rows == 0 or wide >= padded:
+        return
+    first = t.storage_offset()
+    if first + (rows - 1) * stride + padded > t.untyped_storage().nbytes() or (written and first % ROW_PAD):
+        raise ValueError(f"{what}'s rows hold their padding: {padded} values")
+
+
 def _vector(t, n, dtype, what):
     """Address of a contiguous tensor of at least n values."""
     if t.dtype is dtype and t.is_contiguous() and t.numel() >= n:
@@ -652,11 +666,14 @@ def moe_combine_backward(dout, y, slots, weights, dy, dweights, status=None, str
 def quantize_rows(x, q, scales, slots=None, status=None, stream=None):
     """zipccl_quantize_rows: BF16 rows x to int8 rows q (row stride a multiple of ROW_PAD,
     at least as long as x's rows) with float32 scales, to every slot of a token or, without
-    slots, row by row."""
+    slots, row by row.  q is written up to the next multiple of ROW_PAD: rows of fewer columns
+    are taken where they start at a multiple of ROW_PAD in a tensor that goes on that far."""
     xp, T, H, xs = _matrix(x, "x", torch.bfloat16)
     qp, M, wide, qs = _matrix(q, "q", torch.int8)
     if wide < H:
         raise ValueError("q's rows hold x's rows")
+    if wide % ROW_PAD:
+        _holds_padding(q, qs, H, "q", True)
     sp, K = (None, 1) if slots is None else _slots(slots, T)
     _check(_lib.zipccl_quantize_rows(xp, xs, T, H, sp, K, qp, M, qs, _vector(scales, M, torch.float32, "scales"),
                                      _ptr(status), _stream(stream)), "zipccl_quantize_rows")
@@ -675,6 +692,8 @@ def experts_product(q, scales, w, w_scales, row_len: int, out, offsets=None, sta
     _same((om, on), (M, N), "out, and q's rows x w's outputs")
     if row_len > wide or row_len > ws:
         raise ValueError("row_len is at most the row length of q and w")
+    if wide % ROW_PAD:
+        _holds_padding(q, qs, row_len, "q", False)
     _check(_lib.zipccl_experts_product(qp, qs, _vector(scales, M, torch.float32, "scales"), M,
                                        _vector(w, 0, torch.int8, "w"), ws,
                                        _vector(w_scales, E * N, torch.float32, "w_scales"), E, N, row_len,
