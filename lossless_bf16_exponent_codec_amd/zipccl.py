@@ -543,16 +543,17 @@ class Pipeline:
 
 
 # ------------------------------------------------------------------------------------
-# mixture-of-experts rows
+# mixture-of-experts rows: the tensors of a call are on one GPU, and the call is enqueued there
 # ------------------------------------------------------------------------------------
 _DTYPES = {torch.bfloat16: BF16, torch.float32: FP32}
 
 
 def _matrix(t, what, dtype=None):
     """(address, rows, row length, row stride) of a 2-D row-major tensor."""
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{what} is a 2-D tensor")
-    rows, length = t.shape
+    rows, length = shape
     if t.is_contiguous():
         stride = length
     else:
@@ -590,16 +591,56 @@ def _vector(t, n, dtype, what):
 
 def _slots(slots, tokens):
     """(address, top_k) of tokens x top_k slots."""
-    if slots.dim() == 2 and slots.dtype is torch.int32 and slots.is_contiguous():
-        rows, top_k = slots.shape
-        if rows == tokens:
-            return slots.data_ptr(), top_k
+    if slots.dtype is torch.int32 and slots.is_contiguous():
+        shape = slots.shape
+        if len(shape) == 2 and shape[0] == tokens:
+            return slots.data_ptr(), shape[1]
     raise ValueError(f"slots is a contiguous int32 tensor, tokens x top_k, of {tokens} tokens")
 
 
-def _same(a, b, what):
-    if a != b:
-        raise ValueError(f"{what} agree: {a} and {b}")
+def _differ(a, b, what):
+    raise ValueError(f"{what} agree: {a} and {b}")
+
+
+def _enqueue(call, tensors, status, stream, args):
+    """The library's call(*args, status, stream) on the GPU that holds the tensors, on that
+    GPU's current stream if none is given."""
+    device = _current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            device = _one_device(tensors)
+            with torch.cuda.device(device):
+                return _enqueue_on(device, call, status, stream, args)
+    if status is None and stream is None:
+        rc = call(*args, None, _raw_stream(device))
+        if rc != OK:
+            raise ZipcclError(rc, call.__name__)
+    else:
+        _enqueue_on(device, call, status, stream, args)
+
+
+def _one_device(tensors) -> int:
+    """The GPU that holds every tensor that is there (pinned host memory is any GPU's)."""
+    found = {t.get_device() for t in tensors if t is not None and not (t.device.type == "cpu" and t.is_pinned())}
+    if len(found) > 1 or -1 in found:
+        raise ValueError("the tensors are on one GPU")
+    return found.pop() if found else _current_device()
+
+
+def _enqueue_on(device, call, status, stream, args):
+    if status is not None and not isinstance(status, int):
+        other = status.get_device()
+        if other != device and _one_device([status]) != device:
+            _differ(other, device, "the GPUs of status and the other tensors")
+        status = status.data_ptr()
+    if stream is None:
+        stream = _raw_stream(device)
+    elif not isinstance(stream, int):
+        other = getattr(stream, "device_index", device)
+        if other != device:
+            _differ(other, device, "the GPUs of the stream and the tensors")
+        stream = stream.cuda_stream
+    _check(call(*args, status, stream), call.__name__)
 
 
 def moe_sort(experts, num_experts: int, offsets, rows, slots, workspace, status=None, stream=None):
@@ -609,31 +650,32 @@ def moe_sort(experts, num_experts: int, offsets, rows, slots, workspace, status=
     MOE_SORT_WORKSPACE_BYTES device bytes."""
     wide = experts.dtype is torch.int64
     ep, T, K, stride = _matrix(experts, "experts", torch.int64 if wide else torch.int32)
-    _check(_lib.zipccl_moe_sort(ep, 8 if wide else 4, stride, T, K, num_experts,
-                                _vector(offsets, num_experts + 1, torch.int32, "offsets"),
-                                _vector(rows, T * K, torch.int32, "rows"),
-                                _vector(slots, T * K, torch.int32, "slots"), workspace.data_ptr(),
-                                _nbytes(workspace), _ptr(status), _stream(stream)), "zipccl_moe_sort")
+    _enqueue(_lib.zipccl_moe_sort, (experts, offsets, rows, slots, workspace), status, stream,
+             (ep, 8 if wide else 4, stride, T, K, num_experts,
+              _vector(offsets, num_experts + 1, torch.int32, "offsets"), _vector(rows, T * K, torch.int32, "rows"),
+              _vector(slots, T * K, torch.int32, "slots"), workspace.data_ptr(), workspace.nbytes))
 
 
 def moe_dispatch(x, slots, y, status=None, stream=None):
     """zipccl_moe_dispatch: y[slots[t, k]] = x[t]."""
     xp, T, H, xs = _matrix(x, "x")
     yp, M, yh, ys = _matrix(y, "y", x.dtype)
-    _same(H, yh, "the rows of x and y")
+    if H != yh:
+        _differ(H, yh, "the rows of x and y")
     sp, K = _slots(slots, T)
-    _check(_lib.zipccl_moe_dispatch(xp, xs, sp, T, K, H, _DTYPES[x.dtype], yp, M, ys, _ptr(status),
-                                    _stream(stream)), "zipccl_moe_dispatch")
+    _enqueue(_lib.zipccl_moe_dispatch, (x, slots, y), status, stream,
+             (xp, xs, sp, T, K, H, _DTYPES[x.dtype], yp, M, ys))
 
 
 def moe_dispatch_backward(dy, slots, dx, status=None, stream=None):
     """zipccl_moe_dispatch_backward: dx[t] = sum over k of dy[slots[t, k]]."""
     yp, M, H, ys = _matrix(dy, "dy")
     xp, T, xh, xs = _matrix(dx, "dx", dy.dtype)
-    _same(H, xh, "the rows of dy and dx")
+    if H != xh:
+        _differ(H, xh, "the rows of dy and dx")
     sp, K = _slots(slots, T)
-    _check(_lib.zipccl_moe_dispatch_backward(yp, M, ys, sp, T, K, H, _DTYPES[dy.dtype], xp, xs, _ptr(status),
-                                             _stream(stream)), "zipccl_moe_dispatch_backward")
+    _enqueue(_lib.zipccl_moe_dispatch_backward, (dy, slots, dx), status, stream,
+             (yp, M, ys, sp, T, K, H, _DTYPES[dy.dtype], xp, xs))
 
 
 def moe_combine(y, slots, weights, out, status=None, stream=None):
@@ -641,11 +683,12 @@ def moe_combine(y, slots, weights, out, status=None, stream=None):
     float32, or None for 1)."""
     yp, M, H, ys = _matrix(y, "y")
     op, T, oh, os_ = _matrix(out, "out", y.dtype)
-    _same(H, oh, "the rows of y and out")
+    if H != oh:
+        _differ(H, oh, "the rows of y and out")
     sp, K = _slots(slots, T)
     wp = None if weights is None else _vector(weights, T * K, torch.float32, "weights")
-    _check(_lib.zipccl_moe_combine(yp, M, ys, sp, wp, T, K, H, _DTYPES[y.dtype], op, os_, _ptr(status),
-                                   _stream(stream)), "zipccl_moe_combine")
+    _enqueue(_lib.zipccl_moe_combine, (y, slots, weights, out), status, stream,
+             (yp, M, ys, sp, wp, T, K, H, _DTYPES[y.dtype], op, os_))
 
 
 def moe_combine_backward(dout, y, slots, weights, dy, dweights, status=None, stream=None):
@@ -654,13 +697,14 @@ def moe_combine_backward(dout, y, slots, weights, dy, dweights, status=None, str
     gp, T, gh, gs = _matrix(dout, "dout")
     yp, M, H, ys = _matrix(y, "y", dout.dtype)
     dp, dm, dh, ds = _matrix(dy, "dy", dout.dtype)
-    _same(H, gh, "the rows of y and dout")
-    _same((M, H), (dm, dh), "y and dy")
+    if H != gh:
+        _differ(H, gh, "the rows of y and dout")
+    if M != dm or H != dh:
+        _differ((M, H), (dm, dh), "y and dy")
     sp, K = _slots(slots, T)
-    _check(_lib.zipccl_moe_combine_backward(gp, gs, yp, M, ys, sp, _vector(weights, T * K, torch.float32, "weights"),
-                                            T, K, H, _DTYPES[y.dtype], dp, ds,
-                                            _vector(dweights, T * K, torch.float32, "dweights"), _ptr(status),
-                                            _stream(stream)), "zipccl_moe_combine_backward")
+    _enqueue(_lib.zipccl_moe_combine_backward, (dout, y, slots, weights, dy, dweights), status, stream,
+             (gp, gs, yp, M, ys, sp, _vector(weights, T * K, torch.float32, "weights"), T, K, H, _DTYPES[y.dtype],
+              dp, ds, _vector(dweights, T * K, torch.float32, "dweights")))
 
 
 def quantize_rows(x, q, scales, slots=None, status=None, stream=None):
@@ -675,8 +719,8 @@ def quantize_rows(x, q, scales, slots=None, status=None, stream=None):
     if wide % ROW_PAD:
         _holds_padding(q, qs, H, "q", True)
     sp, K = (None, 1) if slots is None else _slots(slots, T)
-    _check(_lib.zipccl_quantize_rows(xp, xs, T, H, sp, K, qp, M, qs, _vector(scales, M, torch.float32, "scales"),
-                                     _ptr(status), _stream(stream)), "zipccl_quantize_rows")
+    _enqueue(_lib.zipccl_quantize_rows, (x, q, scales, slots), status, stream,
+             (xp, xs, T, H, sp, K, qp, M, qs, _vector(scales, M, torch.float32, "scales")))
 
 
 def experts_product(q, scales, w, w_scales, row_len: int, out, offsets=None, status=None, stream=None):
@@ -686,20 +730,21 @@ def experts_product(q, scales, w, w_scales, row_len: int, out, offsets=None, sta
     or float32; offsets: int32, experts + 1 (None: one expert)."""
     qp, M, wide, qs = _matrix(q, "q", torch.int8)
     op, om, on, os_ = _matrix(out, "out")
-    if w.dim() not in (2, 3):
+    shape = w.shape
+    if len(shape) not in (2, 3):
         raise ValueError("w is experts x outputs x row stride")
-    E, N, ws = w.shape if w.dim() == 3 else (1, *w.shape)
-    _same((om, on), (M, N), "out, and q's rows x w's outputs")
+    E, N, ws = shape if len(shape) == 3 else (1, *shape)
+    if om != M or on != N:
+        _differ((om, on), (M, N), "out, and q's rows x w's outputs")
     if row_len > wide or row_len > ws:
         raise ValueError("row_len is at most the row length of q and w")
     if wide % ROW_PAD:
         _holds_padding(q, qs, row_len, "q", False)
-    _check(_lib.zipccl_experts_product(qp, qs, _vector(scales, M, torch.float32, "scales"), M,
-                                       _vector(w, 0, torch.int8, "w"), ws,
-                                       _vector(w_scales, E * N, torch.float32, "w_scales"), E, N, row_len,
-                                       None if offsets is None else _vector(offsets, E + 1, torch.int32, "offsets"),
-                                       op, os_, _DTYPES[out.dtype], _ptr(status), _stream(stream)),
-           "zipccl_experts_product")
+    _enqueue(_lib.zipccl_experts_product, (q, scales, w, w_scales, offsets, out), status, stream,
+             (qp, qs, _vector(scales, M, torch.float32, "scales"), M, _vector(w, 0, torch.int8, "w"), ws,
+              _vector(w_scales, E * N, torch.float32, "w_scales"), E, N, row_len,
+              None if offsets is None else _vector(offsets, E + 1, torch.int32, "offsets"), op, os_,
+              _DTYPES[out.dtype]))
 
 
 # ------------------------------------------------------------------------------------

@@ -9,30 +9,45 @@ NAMES = ("moe_sort", "moe_dispatch", "moe_dispatch_backward", "moe_combine", "mo
 
 
 class Placed(torch.Tensor):
-    """A host tensor that says it lies on GPU `place`."""
+    """A host tensor that says it lies on GPU 0."""
     place = 0
 
     def get_device(self):
         return self.place
 
 
-def placed(t, place=0):
-    t = t.as_subclass(Placed)
-    t.place = place
-    return t
+class Elsewhere(Placed):
+    place = 1
+
+
+def placed(t, place=Placed):
+    return t.as_subclass(place)
 
 
 @pytest.fixture
 def Z(monkeypatch):
-    """The binding with its library's calls recorded in Z.calls: (name, arguments)."""
+    """The binding with its library's calls recorded in Z.calls: (name, arguments,
+    current GPU)."""
     from lossless_bf16_exponent_codec_amd import zipccl
-    calls = []
+    calls, current = [], [0]
     for name in NAMES:
         def record(*args, name=name):
-            calls.append((name, args))
+            calls.append((name, args, current[-1]))
             return zipccl.OK
         monkeypatch.setattr(zipccl.lib(), "zipccl_" + name, record)
-    monkeypatch.setattr(zipccl, "_current_device", lambda: 0)
+
+    class On:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            current.append(self.device)
+
+        def __exit__(self, *_):
+            current.pop()
+
+    monkeypatch.setattr(torch.cuda, "device", On)
+    monkeypatch.setattr(zipccl, "_current_device", lambda: current[-1])
     monkeypatch.setattr(zipccl, "_raw_stream", lambda device: 1000 + device)
     monkeypatch.setattr(zipccl, "calls", calls, raising=False)
     return zipccl
@@ -50,8 +65,8 @@ def quantize(Z, q, length):
 
 def product(Z, q, length):
     M, wide = q.shape[0], -(-length // 128) * 128
-    Z.experts_product(q, placed(torch.zeros(M)), placed(torch.zeros(7, wide, dtype=torch.int8)), placed(torch.zeros(7)), length,
-                      placed(torch.zeros(M, 7)))
+    Z.experts_product(q, placed(torch.zeros(M)), placed(torch.zeros(7, wide, dtype=torch.int8)),
+                      placed(torch.zeros(7)), length, placed(torch.zeros(M, 7)))
 
 
 def test_rows_whose_padding_lies_elsewhere_are_refused(Z):
@@ -77,6 +92,74 @@ def test_rows_with_their_padding_behind_them_are_taken(Z):
     for q in rows8(5, 128), rows8(5, 128, slice(0, 100)), rows8(5, 256, slice(128, 228)), rows8(5, 384, slice(16, 144)):
         quantize(Z, q, 100)
         product(Z, q, 100)
-        assert [name for name, _ in Z.calls] == ["quantize_rows", "experts_product"]
+        assert [name for name, *_ in Z.calls] == ["quantize_rows", "experts_product"]
         assert Z.calls[0][1][6] == q.data_ptr() and Z.calls[0][1][8] == q.stride(0)
+        Z.calls.clear()
+
+
+# Each call as a function of its tensors, by position: (binding, tensors, the rest).
+T, K, E, H, M = 6, 2, 3, 40, 12
+BF = torch.bfloat16
+
+
+def zeros(*shape, dtype=torch.float32):
+    return lambda: torch.zeros(*shape, dtype=dtype)
+
+
+SLOTS, ROWS, TOKENS, WEIGHTS = zeros(T, K, dtype=torch.int32), zeros(M, H, dtype=BF), zeros(T, H, dtype=BF), zeros(T, K)
+ALL = {
+    "moe_sort": (lambda Z, a, **kw: Z.moe_sort(a[0], E, *a[1:], **kw),
+                 [SLOTS, zeros(E + 1, dtype=torch.int32), zeros(M, dtype=torch.int32), SLOTS,
+                  zeros(1 << 20, dtype=torch.uint8)]),
+    "moe_dispatch": (lambda Z, a, **kw: Z.moe_dispatch(*a, **kw), [TOKENS, SLOTS, ROWS]),
+    "moe_dispatch_backward": (lambda Z, a, **kw: Z.moe_dispatch_backward(*a, **kw), [ROWS, SLOTS, TOKENS]),
+    "moe_combine": (lambda Z, a, **kw: Z.moe_combine(*a, **kw), [ROWS, SLOTS, WEIGHTS, TOKENS]),
+    "moe_combine_backward": (lambda Z, a, **kw: Z.moe_combine_backward(*a, **kw),
+                             [TOKENS, ROWS, SLOTS, WEIGHTS, ROWS, WEIGHTS]),
+    "quantize_rows": (lambda Z, a, **kw: Z.quantize_rows(*a[:3], slots=a[3], **kw),
+                      [TOKENS, zeros(M, 128, dtype=torch.int8), zeros(M), SLOTS]),
+    "experts_product": (lambda Z, a, **kw: Z.experts_product(*a[:4], H, a[4], offsets=a[5], **kw),
+                        [zeros(M, 128, dtype=torch.int8), zeros(M), zeros(E, 7, 128, dtype=torch.int8), zeros(E, 7),
+                         zeros(M, 7), zeros(E + 1, dtype=torch.int32)]),
+}
+
+
+@pytest.mark.parametrize("name", ALL)
+def test_tensors_of_the_host_or_of_two_gpus_are_refused(Z, name):
+    call, makers = ALL[name]
+    for place in torch.Tensor, Elsewhere:
+        for i in range(len(makers)):
+            with pytest.raises(ValueError, match="one GPU"):
+                call(Z, [placed(m(), place if j == i else Placed) for j, m in enumerate(makers)])
+    host = [m() for m in makers]
+    with pytest.raises(ValueError, match="one GPU"):
+        call(Z, host)
+    with pytest.raises(ValueError):
+        call(Z, [placed(m()) for m in makers], status=torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        call(Z, [placed(m()) for m in makers], status=placed(torch.zeros(1, dtype=torch.int32), Elsewhere))
+    assert not Z.calls
+
+
+class Stream:
+    def __init__(self, device_index):
+        self.device_index, self.cuda_stream = device_index, 77
+
+
+@pytest.mark.parametrize("name", ALL)
+def test_calls_go_to_the_gpu_that_holds_the_tensors(Z, name):
+    call, makers = ALL[name]
+    for device, place in enumerate((Placed, Elsewhere)):
+        tensors = [placed(m(), place) for m in makers]
+        status = placed(torch.zeros(1, dtype=torch.int32), place)
+        call(Z, tensors)
+        call(Z, tensors, status=status)
+        call(Z, tensors, status=status, stream=Stream(device))
+        call(Z, tensors, status=4096, stream=99)
+        with pytest.raises(ValueError, match="stream"):
+            call(Z, tensors, stream=Stream(1 - device))
+        at = status.data_ptr()
+        assert [(args[-2:], where) for _, args, where in Z.calls] == [
+            ((None, 1000 + device), device), ((at, 1000 + device), device), ((at, 77), device), ((4096, 99), device)]
+        assert all(n == name and args[:-2] == Z.calls[0][1][:-2] for n, args, _ in Z.calls)
         Z.calls.clear()
