@@ -629,6 +629,8 @@ def _one_device(tensors) -> int:
 
 def _enqueue_on(device, call, status, stream, args):
     if status is not None and not isinstance(status, int):
+        if status.nbytes < 4 or not status.is_contiguous():
+            raise ValueError("status is a contiguous tensor of at least 4 bytes")
         other = status.get_device()
         if other != device and _one_device([status]) != device:
             _differ(other, device, "the GPUs of status and the other tensors")
@@ -650,6 +652,8 @@ def moe_sort(experts, num_experts: int, offsets, rows, slots, workspace, status=
     MOE_SORT_WORKSPACE_BYTES device bytes."""
     wide = experts.dtype is torch.int64
     ep, T, K, stride = _matrix(experts, "experts", torch.int64 if wide else torch.int32)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace is contiguous")
     _enqueue(_lib.zipccl_moe_sort, (experts, offsets, rows, slots, workspace), status, stream,
              (ep, 8 if wide else 4, stride, T, K, num_experts,
               _vector(offsets, num_experts + 1, torch.int32, "offsets"), _vector(rows, T * K, torch.int32, "rows"),

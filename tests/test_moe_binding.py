@@ -163,3 +163,19 @@ def test_calls_go_to_the_gpu_that_holds_the_tensors(Z, name):
             ((None, 1000 + device), device), ((at, 1000 + device), device), ((at, 77), device), ((4096, 99), device)]
         assert all(n == name and args[:-2] == Z.calls[0][1][:-2] for n, args, _ in Z.calls)
         Z.calls.clear()
+
+
+def test_workspace_and_status_hold_what_is_written(Z):
+    # 2^20 bytes by their count, one by their memory; a status word of two bytes, and of one
+    # byte four times
+    call, makers = ALL["moe_sort"]
+    tensors = [placed(m()) for m in makers]
+    with pytest.raises(ValueError, match="workspace"):
+        call(Z, tensors[:4] + [placed(torch.zeros(1, dtype=torch.uint8)).expand(1 << 20)])
+    for name, (call, makers) in ALL.items():
+        tensors = [placed(m()) for m in makers]
+        for status in torch.zeros(1, dtype=torch.int16), torch.zeros(0, dtype=torch.int32), \
+                torch.zeros(1, dtype=torch.uint8).expand(4):
+            with pytest.raises(ValueError, match="status"):
+                call(Z, tensors, status=placed(status))
+    assert not Z.calls
