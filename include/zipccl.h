@@ -410,7 +410,7 @@ zipccl_status zipccl_rs_choose(const zipccl_codec_profile_t* prof, const zipccl_
  *     slot (dispatch, combine_backward, quantize_rows) no two choices may share a slot, and
  *     rows no slot names stay as they were.
  *   - tokens == 0 or no rows is valid.  tokens * top_k and the number of rows are below 2^31,
- *     row_len at most 2^28. */
+ *     row_len at most 2^28, strides below 2^40 and rows * stride at most 2^60. */
 #define ZIPCCL_MAX_EXPERTS 1024
 #define ZIPCCL_MAX_TOP_K 64
 #define ZIPCCL_ROW_PAD 128

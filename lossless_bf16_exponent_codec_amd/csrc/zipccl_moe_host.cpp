@@ -22,9 +22,12 @@ constexpr uint64_t kMaxRowLen = 1ull << 28;
 constexpr uint64_t kMaxSumLen = 131071;        // 128 * 128 * this stays below 2^31
 constexpr uint64_t kMaxTiles = 1ull << 24;     // workgroups of one launch
 constexpr uint64_t kMaxByteStride = 1ull << 24;  // of the product's rows: 255 of them stay within 32 bits
-constexpr uint64_t kMaxStride = 1ull << 40;    // keeps row index * stride * 4 within 64 bits
+constexpr uint64_t kMaxStride = 1ull << 40;    // values
+constexpr uint64_t kMaxSpan = 1ull << 60;      // rows * stride: 8 bytes times it stay within 64 bits
 
 bool is_dtype(int d) { return d == ZIPCCL_BF16 || d == ZIPCCL_FP32; }
+// Whether a row stride is too large: by itself, or for the address of the last row.
+bool too_far(uint64_t rows, uint64_t stride) { return stride >= kMaxStride || (rows > 1 && stride > kMaxSpan / rows); }
 uintptr_t value_bytes(int dtype) { return dtype == ZIPCCL_FP32 ? 4 : 2; }
 
 // A matrix of `rows` rows of row_len values at a row stride.
@@ -32,7 +35,7 @@ zipccl_status check_rows(const void* p, uint64_t rows, uint64_t row_len, uint64_
 {
     if (rows > 0 && !p) return ZIPCCL_ERR_INVALID;
     if (rows > 1 && stride < row_len) return ZIPCCL_ERR_INVALID;
-    if (stride >= kMaxStride) return ZIPCCL_ERR_SIZE;
+    if (too_far(rows, stride)) return ZIPCCL_ERR_SIZE;
     if (p && !aligned(p, value_bytes(dtype))) return ZIPCCL_ERR_ALIGN;
     return ZIPCCL_OK;
 }
@@ -78,7 +81,7 @@ zipccl_status zipccl_moe_sort(const void* experts, int id_bytes, uint64_t stride
     if ((id_bytes != 4 && id_bytes != 8) || top_k < 1 || top_k > kMaxTopK || num_experts < 1 ||
         num_experts > kMaxExperts || !offsets || !workspace)
         return ZIPCCL_ERR_INVALID;
-    if (tokens >= kMaxCount || tokens * uint64_t(top_k) >= kMaxCount || stride >= kMaxStride ||
+    if (tokens >= kMaxCount || tokens * uint64_t(top_k) >= kMaxCount || too_far(tokens, stride) ||
         workspace_bytes < kSortWorkspace)
         return ZIPCCL_ERR_SIZE;
     if (tokens > 0 && (!experts || !rows || !slots)) return ZIPCCL_ERR_INVALID;
@@ -206,7 +209,7 @@ zipccl_status zipccl_quantize_rows(const void* x, uint64_t x_stride, uint64_t to
     if (zipccl_status r = check_rows(x, tokens, row_len, x_stride, ZIPCCL_BF16)) return r;
     if (q_rows > 0 && (!q || !scales)) return ZIPCCL_ERR_INVALID;
     if (q_stride < row_len) return ZIPCCL_ERR_INVALID;
-    if (q_stride >= kMaxStride) return ZIPCCL_ERR_SIZE;
+    if (too_far(q_rows, q_stride)) return ZIPCCL_ERR_SIZE;
     if (q_stride % kQuantPad != 0 || !aligned(q, 16) || !aligned(scales, 4)) return ZIPCCL_ERR_ALIGN;
     if (tokens == 0) return ZIPCCL_OK;
     QuantArgs a{};

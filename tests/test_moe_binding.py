@@ -179,3 +179,22 @@ def test_workspace_and_status_hold_what_is_written(Z):
             with pytest.raises(ValueError, match="status"):
                 call(Z, tensors, status=placed(status))
     assert not Z.calls
+
+
+def test_strides_whose_last_row_has_no_64_bit_address_are_refused():
+    # 2^30 rows 2^39 values apart
+    from lossless_bf16_exponent_codec_amd import zipccl as Z
+    L, A, far, many = Z.lib(), 1 << 20, 1 << 39, 1 << 30
+    for rc in (L.zipccl_moe_sort(A, 8, far, many, 1, 4, A, A, A, A, Z.MOE_SORT_WORKSPACE_BYTES, None, None),
+               L.zipccl_moe_dispatch(A, far, A, many, 1, 8, 0, A, 4, 8, None, None),
+               L.zipccl_moe_dispatch(A, 8, A, 4, 1, 8, 1, A, many, far, None, None),
+               L.zipccl_moe_combine(A, many, far, A, A, 4, 1, 8, 0, A, 8, None, None),
+               L.zipccl_moe_combine(A, 4, 8, A, A, many, 1, 8, 1, A, far, None, None),
+               L.zipccl_moe_dispatch_backward(A, many, far, A, 4, 1, 8, 0, A, 8, None, None),
+               L.zipccl_moe_combine_backward(A, far, A, 4, 8, A, A, many, 1, 8, 0, A, 8, A, None, None),
+               L.zipccl_moe_combine_backward(A, 8, A, many, far, A, A, 4, 1, 8, 0, A, 8, A, None, None),
+               L.zipccl_moe_combine_backward(A, 8, A, many, 8, A, A, 4, 1, 8, 0, A, far, A, None, None),
+               L.zipccl_quantize_rows(A, far, many, 8, A, 1, A, 4, 128, A, None, None),
+               L.zipccl_quantize_rows(A, 8, 4, 8, A, 1, A, many, far, A, None, None),
+               L.zipccl_experts_product(A, 128, A, 1 << 24, A, 128, A, 1, 8, 100, None, A, far, 0, None, None)):
+        assert rc == Z.ERR_SIZE
