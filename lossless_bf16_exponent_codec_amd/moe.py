@@ -3,14 +3,15 @@ sorted by expert, tokens dispatched to their experts' rows and combined back wit
 (differentiable), and experts' weights in 8 bits.
 
 Each step is one call of the same name in `zipccl`; this module adds the buffers and the
-gradients.  `examples/moe_exchange.py` runs the whole path, the compressed exchange
-between ranks included.
+gradients (of first order).  `examples/moe_exchange.py` runs the whole path, the
+compressed exchange between ranks included.
 """
 from __future__ import annotations
 
 from dataclasses import dataclass
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import zipccl as Z
 
@@ -50,6 +51,7 @@ class _Dispatch(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable   # the kernels write past autograd: a second derivative is an error
     def backward(ctx, dy):
         slots, = ctx.saved_tensors
         dx = dy.new_empty(slots.shape[0], dy.shape[1])
@@ -66,6 +68,7 @@ class _Combine(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable   # the kernels write past autograd: a second derivative is an error
     def backward(ctx, dout):
         y, slots, weights = ctx.saved_tensors
         dy, dw = torch.zeros_like(y), torch.empty_like(weights)   # zeros: rows that no choice names

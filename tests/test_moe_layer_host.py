@@ -1,0 +1,81 @@
+"""The torch layer of the mixture-of-experts calls on the CPU: the calls themselves are
+stand-ins in plain torch, so that what is tested is the layer's buffers, gradients and
+refusals."""
+import pytest
+import torch
+
+
+def picked(rows, slots):
+    kept = ((slots >= 0) & (slots < rows.shape[0])).unsqueeze(-1)
+    return torch.where(kept, rows[slots.clamp(0, max(rows.shape[0] - 1, 0)).long()], torch.zeros(()))
+
+
+def sort(experts, num_experts, offsets, rows, slots, workspace, status=None):
+    flat = torch.where(experts < 0, num_experts, experts).reshape(-1)
+    order = torch.sort(flat, stable=True)
+    offsets.copy_(torch.searchsorted(order.values, torch.arange(num_experts + 1)))
+    rows.copy_(torch.where(order.values < num_experts, order.indices // experts.shape[1], -1))
+    place = torch.empty_like(flat)
+    place[order.indices] = torch.arange(flat.numel())
+    slots.copy_(torch.where(flat < num_experts, place, -1).view(experts.shape))
+
+
+def dispatch(x, slots, y, status=None):
+    for t, k in (slots >= 0).nonzero().tolist():
+        if slots[t, k] < y.shape[0]:
+            y[slots[t, k]] = x[t]
+        elif status is not None:
+            status |= 4
+
+
+def combine(y, slots, weights, out, status=None):
+    w = torch.ones(slots.shape) if weights is None else weights
+    out.copy_((w.unsqueeze(-1) * picked(y, slots)).sum(1))
+    if status is not None and bool((slots >= y.shape[0]).any()):
+        status |= 4
+
+
+def combine_backward(dout, y, slots, weights, dy, dweights, status=None):
+    dweights.copy_((dout.unsqueeze(1) * picked(y, slots)).sum(-1))
+    for t, k in (slots >= 0).nonzero().tolist():
+        if slots[t, k] < y.shape[0]:
+            dy[slots[t, k]] = weights[t, k] * dout[t]
+        elif status is not None:
+            status |= 4
+
+
+@pytest.fixture
+def moe(monkeypatch):
+    from lossless_bf16_exponent_codec_amd import moe
+
+    def dispatch_backward(dy, slots, dx, status=None):
+        combine(dy, slots, None, dx, status)
+
+    for name, plain in dict(moe_sort=sort, moe_dispatch=dispatch, moe_dispatch_backward=dispatch_backward,
+                            moe_combine=combine, moe_combine_backward=combine_backward).items():
+        monkeypatch.setattr(moe.Z, name, torch.no_grad()(plain))   # autograd does not see what a kernel writes
+    return moe
+
+
+IDS = torch.tensor([[0, 2], [1, -1], [2, 0]])
+
+
+def test_second_order_gradients_are_an_error_not_zero(moe):
+    # the gradients are written by kernels that autograd does not see: differentiating them
+    # again has to fail, not to drop the terms
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(3, 4, generator=g, requires_grad=True)
+    w = torch.rand(3, 2, generator=g, requires_grad=True)
+    routing = moe.route(IDS, 3)
+    M = routing.splits()[-1]
+    y = moe.dispatch(x, routing, M)
+    dx, = torch.autograd.grad((y ** 2).sum(), x, create_graph=True)
+    assert torch.equal(dx.detach(), 2 * x.detach() * torch.tensor([[2.0], [1.0], [2.0]]))
+    with pytest.raises(RuntimeError, match="twice"):
+        (dx ** 2).sum().backward()
+    rows = torch.randn(M, 4, generator=g, requires_grad=True)
+    out = moe.combine(rows, routing, w)
+    for leaf in rows, w:
+        grad, = torch.autograd.grad((out ** 2).sum(), leaf, create_graph=True)
+        with pytest.raises(RuntimeError, match="twice"):
+            (out.sum() + (grad ** 2).sum()).backward(retain_graph=True)
