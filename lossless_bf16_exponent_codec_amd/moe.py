@@ -106,7 +106,8 @@ def quantize(x: torch.Tensor, slots=None, nrows: int | None = None) -> Quantized
 
 class QuantizedExperts:
     """Weights of all experts (experts x outputs x inputs, BF16) laid out once in 8 bits
-    with a scale per output channel.  Calling it multiplies rows sorted by expert."""
+    with a scale per output channel.  Calling it multiplies rows (of `inputs` values) sorted
+    by expert."""
 
     def __init__(self, weights: torch.Tensor):
         self.experts, self.outputs, self.inputs = weights.shape
@@ -115,6 +116,8 @@ class QuantizedExperts:
         self.scales = rows.scales.view(self.experts, self.outputs)
 
     def __call__(self, rows: QuantizedRows, routing: Routing, dtype=torch.bfloat16) -> torch.Tensor:
+        if rows.row_len != self.inputs:
+            raise ValueError(f"rows of {rows.row_len} values, experts of {self.inputs} inputs")
         out = torch.empty(rows.q.shape[0], self.outputs, dtype=dtype, device=rows.q.device)
         Z.experts_product(rows.q, rows.scales, self.q, self.scales, self.inputs, out, offsets=routing.offsets)
         return out

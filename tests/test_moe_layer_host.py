@@ -79,3 +79,17 @@ def test_second_order_gradients_are_an_error_not_zero(moe):
         grad, = torch.autograd.grad((out ** 2).sum(), leaf, create_graph=True)
         with pytest.raises(RuntimeError, match="twice"):
             (out.sum() + (grad ** 2).sum()).backward(retain_graph=True)
+
+
+def test_products_of_rows_of_another_length_are_refused(moe, monkeypatch):
+    asked = []
+    monkeypatch.setattr(moe.Z, "quantize_rows", lambda *a, **kw: None)
+    monkeypatch.setattr(moe.Z, "experts_product", lambda *a, **kw: asked.append(a))
+    experts = moe.QuantizedExperts(torch.zeros(3, 5, 250, dtype=torch.bfloat16))
+    routing = moe.route(IDS, 3)
+    for length in 200, 249, 256, 1000:
+        with pytest.raises(ValueError, match="250"):
+            experts(moe.quantize(torch.zeros(5, length, dtype=torch.bfloat16)), routing)
+    assert not asked
+    experts(moe.quantize(torch.zeros(5, 250, dtype=torch.bfloat16)), routing)
+    assert len(asked) == 1
