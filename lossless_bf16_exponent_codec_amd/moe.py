@@ -118,6 +118,8 @@ class QuantizedExperts:
     def __call__(self, rows: QuantizedRows, routing: Routing, dtype=torch.bfloat16) -> torch.Tensor:
         if rows.row_len != self.inputs:
             raise ValueError(f"rows of {rows.row_len} values, experts of {self.inputs} inputs")
+        if routing.offsets.numel() != self.experts + 1:
+            raise ValueError(f"{routing.offsets.numel()} offsets, {self.experts} experts")
         out = torch.empty(rows.q.shape[0], self.outputs, dtype=dtype, device=rows.q.device)
         Z.experts_product(rows.q, rows.scales, self.q, self.scales, self.inputs, out, offsets=routing.offsets)
         return out

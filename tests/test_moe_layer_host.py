@@ -93,3 +93,18 @@ def test_products_of_rows_of_another_length_are_refused(moe, monkeypatch):
     assert not asked
     experts(moe.quantize(torch.zeros(5, 250, dtype=torch.bfloat16)), routing)
     assert len(asked) == 1
+
+
+def test_products_with_offsets_of_other_experts_are_refused(moe, monkeypatch):
+    # with more offsets than experts the rows of the others would be memory as it was found
+    asked = []
+    monkeypatch.setattr(moe.Z, "quantize_rows", lambda *a, **kw: None)
+    monkeypatch.setattr(moe.Z, "experts_product", lambda *a, **kw: asked.append(a))
+    experts = moe.QuantizedExperts(torch.zeros(3, 5, 250, dtype=torch.bfloat16))
+    rows = moe.quantize(torch.zeros(5, 250, dtype=torch.bfloat16))
+    for other in 2, 4:
+        with pytest.raises(ValueError, match="experts"):
+            experts(rows, moe.route(IDS.clamp(max=1), other))
+    assert not asked
+    experts(rows, moe.route(IDS, 3))
+    assert len(asked) == 1
