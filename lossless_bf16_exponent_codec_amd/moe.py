@@ -21,15 +21,19 @@ __all__ = ["Routing", "route", "dispatch", "combine", "QuantizedRows", "quantize
 @dataclass
 class Routing:
     """Choices sorted by expert: rows[offsets[e]:offsets[e + 1]] are the tokens of expert
-    e's rows, slots[t, k] the row of token t's k-th choice (-1: dropped)."""
+    e's rows, slots[t, k] the row of token t's k-th choice (-1: dropped).  The tensors are
+    one sort's: another sort makes another routing."""
     offsets: torch.Tensor
     rows: torch.Tensor
     slots: torch.Tensor
+    kept: int | None = None   # number of rows, once splits() has brought it to the host
 
     def splits(self) -> list:
         """The offsets on the host (waits for the sort): sizes of buffers and of the
         all-to-all.  The last one is the number of rows."""
-        return self.offsets.tolist()
+        ends = self.offsets.tolist()
+        self.kept = ends[-1]
+        return ends
 
 
 def route(experts: torch.Tensor, num_experts: int, status=None) -> Routing:
@@ -44,9 +48,14 @@ def route(experts: torch.Tensor, num_experts: int, status=None) -> Routing:
 
 class _Dispatch(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, slots, nrows):
+    def forward(ctx, x, slots, nrows, kept):
         ctx.save_for_backward(slots)
-        y = x.new_empty(nrows, x.shape[1])
+        if kept is None:
+            y = x.new_zeros(nrows, x.shape[1])
+        else:
+            y = x.new_empty(nrows, x.shape[1])
+            if kept < nrows:
+                y[kept:].zero_()
         Z.moe_dispatch(x, slots, y)
         return y
 
@@ -56,7 +65,7 @@ class _Dispatch(torch.autograd.Function):
         slots, = ctx.saved_tensors
         dx = dy.new_empty(slots.shape[0], dy.shape[1])
         Z.moe_dispatch_backward(dy.contiguous(), slots, dx)
-        return dx, None, None
+        return dx, None, None, None
 
 
 class _Combine(torch.autograd.Function):
@@ -77,8 +86,10 @@ class _Combine(torch.autograd.Function):
 
 
 def dispatch(x: torch.Tensor, routing: Routing, nrows: int) -> torch.Tensor:
-    """Rows by expert (nrows = routing.splits()[-1]) of the tokens x; differentiable in x."""
-    return _Dispatch.apply(x, routing.slots, nrows)
+    """Rows by expert of the tokens x; differentiable in x.  nrows: routing.splits()[-1], or
+    a fixed number of rows, of which those that no choice has are zero (before splits() all
+    are cleared first, since which they are is not known here)."""
+    return _Dispatch.apply(x, routing.slots, nrows, routing.kept)
 
 
 def combine(y: torch.Tensor, routing: Routing, weights: torch.Tensor) -> torch.Tensor:
@@ -96,7 +107,8 @@ class QuantizedRows:
 
 
 def quantize(x: torch.Tensor, slots=None, nrows: int | None = None) -> QuantizedRows:
-    """BF16 rows in 8 bits: row by row, or each token's to its slots among nrows rows."""
+    """BF16 rows in 8 bits: row by row, or each token's to its slots among nrows rows (those
+    that no choice has, and their products, are not set)."""
     n, wide = x.shape[0] if slots is None else nrows, -(-x.shape[1] // Z.ROW_PAD) * Z.ROW_PAD
     r = QuantizedRows(torch.empty(n, wide, dtype=torch.int8, device=x.device),
                       torch.empty(n, dtype=torch.float32, device=x.device), x.shape[1])

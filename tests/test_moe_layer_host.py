@@ -108,3 +108,33 @@ def test_products_with_offsets_of_other_experts_are_refused(moe, monkeypatch):
     assert not asked
     experts(rows, moe.route(IDS, 3))
     assert len(asked) == 1
+
+
+@pytest.fixture
+def poison():
+    """Memory that is not written holds NaN (whole numbers: their largest)."""
+    torch.use_deterministic_algorithms(True)
+    yield
+    torch.use_deterministic_algorithms(False)
+
+
+def test_rows_of_no_choice_are_zero(moe, poison):
+    # 5 kept choices in a buffer of 8 rows, with the kept count on the host and without: the
+    # rows past them are read by a dense expert and by its weights' gradient
+    g = torch.Generator().manual_seed(3)
+    x, f = torch.randn(3, 4, generator=g), torch.randn(4, 4, generator=g)
+    assert bool(torch.empty(3).isnan().all())
+    for count_first in True, False:
+        routing = moe.route(IDS, 3)
+        if count_first:
+            assert routing.splits() == [0, 2, 3, 5]
+        xs, fs = x.clone().requires_grad_(), f.clone().requires_grad_()
+        y = moe.dispatch(xs, routing, 8)
+        assert not y[5:].any() and torch.equal(y[:5], x[[0, 2, 1, 0, 2]])
+        out = moe.combine(y @ fs, routing, torch.ones(3, 2))
+        out.sum().backward()
+        kept = torch.tensor([[2.0], [1.0], [2.0]])
+        torch.testing.assert_close(fs.grad, (kept * x).sum(0).unsqueeze(1).expand(4, 4))
+        torch.testing.assert_close(xs.grad, kept * f.sum(1))
+        # no rows past the kept ones: nothing to clear
+        assert torch.equal(moe.dispatch(x, routing, 5), x[[0, 2, 1, 0, 2]])
