@@ -56,19 +56,19 @@ def step(tokens=4096, hidden=1024, inner=512, experts=16, top_k=2, ranks=8, seed
     sent, there = send([(x, routing.rows[a:b], plan) for a, b in cuts], cuts, hidden, status)
 
     # the experts' two products
-    inside = torch.nn.functional.silu(w1(moe.quantize(sent), routing))
-    made = w2(moe.quantize(inside), routing)
+    inside = torch.nn.functional.silu(w1(moe.quantize(sent), routing, status=status))
+    made = w2(moe.quantize(inside), routing, status=status)
 
     # and back: each rank's rows as they lie
     scale = float(made.float().std())
     back, home = send([(made[a:b].reshape(-1), Z.plan(sigma=scale)) for a, b in cuts], cuts, hidden, status)
-    out = moe.combine(back, routing, weights)
+    out = moe.combine(back, routing, weights, status)
 
     # gradients: of the combine (rows and weights), and of the dispatch
     y, w, xg = back.detach().requires_grad_(), weights.detach().requires_grad_(), x.detach().requires_grad_()
     dout = torch.randn(tokens, hidden, generator=g, device="cuda").bfloat16()
-    dy, dw = torch.autograd.grad(moe.combine(y, routing, w), (y, w), dout)
-    dx, = torch.autograd.grad(moe.dispatch(xg, routing, ends[-1]), xg, dy)
+    dy, dw = torch.autograd.grad(moe.combine(y, routing, w, status), (y, w), dout)
+    dx, = torch.autograd.grad(moe.dispatch(xg, routing, ends[-1], status), xg, dy)
     return dict(x=x, w1=w1, w2=w2, weights=weights, routing=routing, ends=ends, sent=sent, made=made, back=back,
                 out=out, dout=dout, dy=dy, dw=dw, dx=dx, status=int(status.item()),
                 ratio=2 * 2 * ends[-1] * hidden / (there + home))

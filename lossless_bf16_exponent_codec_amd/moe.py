@@ -3,8 +3,10 @@ sorted by expert, tokens dispatched to their experts' rows and combined back wit
 (differentiable), and experts' weights in 8 bits.
 
 Each step is one call of the same name in `zipccl`; this module adds the buffers and the
-gradients (of first order).  `examples/moe_exchange.py` runs the whole path, the
-compressed exchange between ranks included.
+gradients (of first order).  A status word (int32, on the device) given to a step takes the
+bits that its calls set, those of its gradient among them: STATUS_BAD_INDEX for a choice that
+was dropped because its expert or its row is out of range.  `examples/moe_exchange.py` runs
+the whole path, the compressed exchange between ranks included.
 """
 from __future__ import annotations
 
@@ -48,15 +50,16 @@ def route(experts: torch.Tensor, num_experts: int, status=None) -> Routing:
 
 class _Dispatch(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, slots, nrows, kept):
+    def forward(ctx, x, slots, nrows, kept, status):
         ctx.save_for_backward(slots)
+        ctx.status = status
         if kept is None:
             y = x.new_zeros(nrows, x.shape[1])
         else:
             y = x.new_empty(nrows, x.shape[1])
             if kept < nrows:
                 y[kept:].zero_()
-        Z.moe_dispatch(x, slots, y)
+        Z.moe_dispatch(x, slots, y, status)
         return y
 
     @staticmethod
@@ -64,16 +67,17 @@ class _Dispatch(torch.autograd.Function):
     def backward(ctx, dy):
         slots, = ctx.saved_tensors
         dx = dy.new_empty(slots.shape[0], dy.shape[1])
-        Z.moe_dispatch_backward(dy.contiguous(), slots, dx)
-        return dx, None, None, None
+        Z.moe_dispatch_backward(dy.contiguous(), slots, dx, ctx.status)
+        return dx, None, None, None, None
 
 
 class _Combine(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, y, slots, weights):
+    def forward(ctx, y, slots, weights, status):
         ctx.save_for_backward(y, slots, weights)
+        ctx.status = status
         out = y.new_empty(slots.shape[0], y.shape[1])
-        Z.moe_combine(y, slots, weights, out)
+        Z.moe_combine(y, slots, weights, out, status)
         return out
 
     @staticmethod
@@ -81,21 +85,21 @@ class _Combine(torch.autograd.Function):
     def backward(ctx, dout):
         y, slots, weights = ctx.saved_tensors
         dy, dw = torch.zeros_like(y), torch.empty_like(weights)   # zeros: rows that no choice names
-        Z.moe_combine_backward(dout.contiguous(), y, slots, weights, dy, dw)
-        return dy, None, dw
+        Z.moe_combine_backward(dout.contiguous(), y, slots, weights, dy, dw, ctx.status)
+        return dy, None, dw, None
 
 
-def dispatch(x: torch.Tensor, routing: Routing, nrows: int) -> torch.Tensor:
+def dispatch(x: torch.Tensor, routing: Routing, nrows: int, status=None) -> torch.Tensor:
     """Rows by expert of the tokens x; differentiable in x.  nrows: routing.splits()[-1], or
     a fixed number of rows, of which those that no choice has are zero (before splits() all
     are cleared first, since which they are is not known here)."""
-    return _Dispatch.apply(x, routing.slots, nrows, routing.kept)
+    return _Dispatch.apply(x, routing.slots, nrows, routing.kept, status)
 
 
-def combine(y: torch.Tensor, routing: Routing, weights: torch.Tensor) -> torch.Tensor:
+def combine(y: torch.Tensor, routing: Routing, weights: torch.Tensor, status=None) -> torch.Tensor:
     """Tokens from rows by expert: sums with weights (float32, tokens x top_k);
     differentiable in y and weights."""
-    return _Combine.apply(y, routing.slots, weights.contiguous())
+    return _Combine.apply(y, routing.slots, weights.contiguous(), status)
 
 
 @dataclass
@@ -106,13 +110,13 @@ class QuantizedRows:
     row_len: int
 
 
-def quantize(x: torch.Tensor, slots=None, nrows: int | None = None) -> QuantizedRows:
+def quantize(x: torch.Tensor, slots=None, nrows: int | None = None, status=None) -> QuantizedRows:
     """BF16 rows in 8 bits: row by row, or each token's to its slots among nrows rows (those
     that no choice has, and their products, are not set)."""
     n, wide = x.shape[0] if slots is None else nrows, -(-x.shape[1] // Z.ROW_PAD) * Z.ROW_PAD
     r = QuantizedRows(torch.empty(n, wide, dtype=torch.int8, device=x.device),
                       torch.empty(n, dtype=torch.float32, device=x.device), x.shape[1])
-    Z.quantize_rows(x, r.q, r.scales, slots=slots)
+    Z.quantize_rows(x, r.q, r.scales, slots=slots, status=status)
     return r
 
 
@@ -127,11 +131,12 @@ class QuantizedExperts:
         self.q = rows.q.view(self.experts, self.outputs, -1)
         self.scales = rows.scales.view(self.experts, self.outputs)
 
-    def __call__(self, rows: QuantizedRows, routing: Routing, dtype=torch.bfloat16) -> torch.Tensor:
+    def __call__(self, rows: QuantizedRows, routing: Routing, dtype=torch.bfloat16, status=None) -> torch.Tensor:
         if rows.row_len != self.inputs:
             raise ValueError(f"rows of {rows.row_len} values, experts of {self.inputs} inputs")
         if routing.offsets.numel() != self.experts + 1:
             raise ValueError(f"{routing.offsets.numel()} offsets, {self.experts} experts")
         out = torch.empty(rows.q.shape[0], self.outputs, dtype=dtype, device=rows.q.device)
-        Z.experts_product(rows.q, rows.scales, self.q, self.scales, self.inputs, out, offsets=routing.offsets)
+        Z.experts_product(rows.q, rows.scales, self.q, self.scales, self.inputs, out, offsets=routing.offsets,
+                          status=status)
         return out

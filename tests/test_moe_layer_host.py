@@ -138,3 +138,31 @@ def test_rows_of_no_choice_are_zero(moe, poison):
         torch.testing.assert_close(xs.grad, kept * f.sum(1))
         # no rows past the kept ones: nothing to clear
         assert torch.equal(moe.dispatch(x, routing, 5), x[[0, 2, 1, 0, 2]])
+
+
+def test_status_word_of_each_call(moe, monkeypatch):
+    # slots past the rows are dropped; the caller's status word says so, forward and backward
+    for name in "quantize_rows", "experts_product":
+        monkeypatch.setattr(moe.Z, name, lambda *a, status=None, **kw: status is None or status.fill_(64))
+    routing = moe.route(IDS, 3)
+    x = torch.zeros(3, 4, requires_grad=True)
+    status = torch.zeros(1, dtype=torch.int32)
+    y = moe.dispatch(x, routing, 4, status)
+    assert int(status) == 4
+    status.zero_()
+    y.sum().backward()
+    assert int(status) == 4
+    rows = torch.zeros(4, 4, requires_grad=True)
+    status.zero_()
+    out = moe.combine(rows, routing, torch.ones(3, 2), status)
+    assert int(status) == 4
+    status.zero_()
+    out.sum().backward()
+    assert int(status) == 4
+    moe.quantize(torch.zeros(3, 250, dtype=torch.bfloat16), routing.slots, 4, status)
+    assert int(status) == 64
+    status.zero_()
+    status.zero_()
+    experts = moe.QuantizedExperts(torch.zeros(3, 5, 250, dtype=torch.bfloat16))
+    experts(moe.QuantizedRows(torch.zeros(4, 256, dtype=torch.int8), torch.zeros(4), 250), routing, status=status)
+    assert int(status) == 64
