@@ -163,12 +163,18 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+try:   # the handle alone: building a torch.cuda.Stream takes 3 us, as long as a launch
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+    from torch._C import _cuda_getDevice as _current_device
+except ImportError:   # a torch that has no such call (one built without GPU support)
+    _current_device = torch.cuda.current_device
+
+    def _raw_stream(device: int) -> int:
+        return torch.cuda.current_stream(device).cuda_stream
 
 
 def _stream(stream) -> int | None:
     if stream is None:
-        # the handle alone: building a torch.cuda.Stream takes 3 us, as long as a launch
         return _raw_stream(_current_device())
     if isinstance(stream, int):
         return stream

@@ -198,3 +198,17 @@ def test_strides_whose_last_row_has_no_64_bit_address_are_refused():
                L.zipccl_quantize_rows(A, 8, 4, 8, A, 1, A, many, far, A, None, None),
                L.zipccl_experts_product(A, 128, A, 1 << 24, A, 128, A, 1, 8, 100, None, A, far, 0, None, None)):
         assert rc == Z.ERR_SIZE
+
+
+def test_host_calls_need_no_gpu_build_of_torch():
+    # a torch without GPU support has no call for a stream's handle: the package loads, and
+    # its host calls work
+    import subprocess
+    import sys
+    code = ("import torch\n"
+            "for name in '_cuda_getCurrentRawStream', '_cuda_getDevice':\n"
+            "    if hasattr(torch._C, name): delattr(torch._C, name)\n"
+            "from lossless_bf16_exponent_codec_amd import zipccl as Z\n"
+            "assert Z.static_size(100) > 0 and len(Z.plan(sigma=1.0).exponents) == 7\n")
+    root = __file__.rsplit("/tests/", 1)[0]
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root, timeout=300)
