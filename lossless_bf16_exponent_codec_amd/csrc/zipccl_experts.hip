@@ -592,6 +592,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void product_split_kernel(const Pr
     const uint32_t across = (a.outputs + kSplitOuts - 1) / kSplitOuts;
     uint32_t expert, row0, rows;
     RowTiles<64> map(a);
+    if (a.experts > 64 && blockIdx.x == 0) map.count(a);   // one workgroup looks at every offset, for the status
     if (!map.find(a, blockIdx.x / across, expert, row0, rows)) return;
     const uint32_t n0 = blockIdx.x % across * kSplitOuts;
     const uint32_t tid = threadIdx.x, lane = lane_id();

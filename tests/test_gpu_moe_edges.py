@@ -1,0 +1,77 @@
+"""Mixture-of-experts operators on the GPU where calls are largest and where their inputs are
+wrong: loops over more work than a grid has workgroups, offsets that are out of range, NaN
+scales, rows that no choice has.  Tolerances as in the other tests of these operators: a value
+rounded once to BF16 is off by at most 2^-8 of it, an fp32 sum of n terms by at most n * 2^-23
+of the sum of their magnitudes; whole numbers are equal."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF16_REL = 2.0 ** -8
+SHAPES = [  # experts, rows, outputs, row length: a call of each tile shape
+    (4, 50, 40, 256), (128, 1, 40, 200), (128, 40, 40, 130), (70, 3000, 300, 200), (70, 3000, 700, 200),
+    (70, 9000, 300, 200), (5, 9000, 300, 200), (100, 22000, 1024, 2048)]
+
+
+@pytest.fixture(scope="module")
+def Z():
+    from lossless_bf16_exponent_codec_amd import zipccl
+    return zipccl
+
+
+def operands(E, M, N, H):
+    g = torch.Generator(device="cuda").manual_seed(E + M + N)
+    wide = -(-H // 128) * 128
+    q = torch.zeros(M, wide, dtype=torch.int8, device="cuda")
+    w = torch.zeros(E, N, wide, dtype=torch.int8, device="cuda")
+    q[:, :H] = torch.randint(-127, 128, (M, H), generator=g, device="cuda", dtype=torch.int8)
+    w[:, :, :H] = torch.randint(-127, 128, (E, N, H), generator=g, device="cuda", dtype=torch.int8)
+    return q, torch.rand(M, generator=g, device="cuda") + 0.5, w, torch.rand(E, N, generator=g, device="cuda") + 0.5
+
+
+def even(E, M):
+    return [M * e // E for e in range(E + 1)]
+
+
+@pytest.mark.parametrize("E,M,N,H", SHAPES)
+def test_every_offset_out_of_range_is_reported(Z, E, M, N, H):
+    q, scales, w, w_scales = operands(E, M, N, H)
+    good = even(E, M)
+
+    def run(offsets):
+        out = torch.full((M, N), 12345.0, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        Z.experts_product(q, scales, w, w_scales, H, out, status=status,
+                          offsets=torch.tensor(offsets, dtype=torch.int32, device="cuda"))
+        return out, int(status.item())
+
+    def check(out, offsets):
+        held = torch.zeros(M, dtype=torch.bool)
+        for e in range(E):
+            a, b = offsets[e], offsets[e + 1]
+            if a < b:
+                held[a:b] = True
+                sums = q[a:b].double() @ w[e].double().t().contiguous()
+                want = sums * scales[a:b, None].double() * w_scales[e].double()
+                assert bool(((out[a:b].double() - want).abs() <= 4 * 2.0 ** -24 * want.abs()).all())
+        assert bool((out[~held.cuda()] == 12345.0).all())
+
+    out, status = run(good)
+    assert status == 0
+    check(out, good)
+    for at in 0, E // 3, E - 1, E:   # out of range, the others ascending where they are clamped
+        for value in -5, M + 1000:
+            offsets = [min(v, value) if i < at else max(v, value) if i > at else value for i, v in enumerate(good)]
+            out, status = run(offsets)
+            assert status == Z.STATUS_BAD_INDEX, (at, value)
+            check(out, [min(max(v, 0), M) for v in offsets])
+    for rest in good, [0] + [M] * E:  # one alone; the rows with all experts or with the first
+        for at in 1, E // 3 + 1, E - 1:
+            for value in -5, M + 1000:
+                offsets = list(rest)
+                offsets[at] = value
+                assert run(offsets)[1] == Z.STATUS_BAD_INDEX, (rest[1], at, value)
+    for at in 0, E // 3, E - 1:      # in range, descending
+        offsets = [M] * (at + 1) + [0] + [M] * (E - at - 1)
+        assert run(offsets)[1] == Z.STATUS_BAD_INDEX, at
