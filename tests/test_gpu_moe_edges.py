@@ -75,3 +75,22 @@ def test_every_offset_out_of_range_is_reported(Z, E, M, N, H):
     for at in 0, E // 3, E - 1:      # in range, descending
         offsets = [M] * (at + 1) + [0] + [M] * (E - at - 1)
         assert run(offsets)[1] == Z.STATUS_BAD_INDEX, at
+
+
+@pytest.mark.parametrize("E,M,N,H", SHAPES)
+def test_nan_products_are_one_bit_pattern(Z, E, M, N, H):
+    # NaNs of either sign and any payload, quiet and signalling, in rows' and channels' scales,
+    # and infinity times zero: 0x7FC0 in BF16
+    q, scales, w, w_scales = operands(E, M, N, H)
+    nans = torch.tensor([-0x400000, 0x7FFFFFFF, 0x7FA12345, 0x7F800001, -1], dtype=torch.int32, device="cuda")   # bits
+    rows, zero_rows, columns = slice(0, M, 7), slice(3, M, 7), slice(1, N, 9)
+    scales.view(torch.int32)[rows] = nans[torch.arange(0, M, 7, device="cuda") % 5]
+    w_scales.view(torch.int32)[:, columns] = nans[torch.arange(1, N, 9, device="cuda") % 5]
+    q[zero_rows], scales[zero_rows] = 0, float("inf")
+    out = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    Z.experts_product(q, scales, w, w_scales, H, out,
+                      offsets=torch.tensor(even(E, M), dtype=torch.int32, device="cuda"))
+    want = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    want[rows], want[:, columns], want[zero_rows] = True, True, True
+    assert bool((out.view(torch.int16)[want] == 0x7FC0).all())
+    assert bool(out[~want].isfinite().all())
