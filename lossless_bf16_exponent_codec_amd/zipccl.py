@@ -551,11 +551,15 @@ class Pipeline:
 # ------------------------------------------------------------------------------------
 # mixture-of-experts rows: the tensors of a call are on one GPU, and the call is enqueued there
 # ------------------------------------------------------------------------------------
-_DTYPES = {torch.bfloat16: BF16, torch.float32: FP32}
+_VALUES = {torch.bfloat16: BF16, torch.float32: FP32}
+_IDS = {torch.int32: 4, torch.int64: 8}
+_BF16_ONLY = {torch.bfloat16: BF16}
+_INT8 = {torch.int8: 1}
 
 
-def _matrix(t, what, dtype=None):
-    """(address, rows, row length, row stride) of a 2-D row-major tensor."""
+def _matrix(t, what, kinds=_VALUES):
+    """(address, rows, row length, row stride, kind) of a 2-D row-major tensor; kinds: the
+    types it may have, and what the library calls them."""
     shape = t.shape
     if len(shape) != 2:
         raise ValueError(f"{what} is a 2-D tensor")
@@ -569,9 +573,10 @@ def _matrix(t, what, dtype=None):
         if rows > 1 and stride < length:
             raise ValueError(f"{what} has rows that do not overlap")
         stride = max(stride, length)
-    if t.dtype is not dtype and (dtype is not None or t.dtype not in _DTYPES):
+    kind = kinds.get(t.dtype)
+    if kind is None:
         raise ValueError(f"{what} is {t.dtype}")
-    return t.data_ptr(), rows, length, stride
+    return t.data_ptr(), rows, length, stride, kind
 
 
 def _holds_padding(t, stride, row_len, what, written):
@@ -613,7 +618,7 @@ def _enqueue(call, tensors, status, stream, args):
     GPU's current stream if none is given."""
     device = _current_device()
     for t in tensors:
-        if t is not None and t.get_device() != device:
+        if t.get_device() != device:
             device = _one_device(tensors)
             with torch.cuda.device(device):
                 return _enqueue_on(device, call, status, stream, args)
@@ -626,8 +631,8 @@ def _enqueue(call, tensors, status, stream, args):
 
 
 def _one_device(tensors) -> int:
-    """The GPU that holds every tensor that is there (pinned host memory is any GPU's)."""
-    found = {t.get_device() for t in tensors if t is not None and not (t.device.type == "cpu" and t.is_pinned())}
+    """The GPU that holds every tensor (pinned host memory is any GPU's)."""
+    found = {t.get_device() for t in tensors if not (t.device.type == "cpu" and t.is_pinned())}
     if len(found) > 1 or -1 in found:
         raise ValueError("the tensors are on one GPU")
     return found.pop() if found else _current_device()
@@ -656,64 +661,64 @@ def moe_sort(experts, num_experts: int, offsets, rows, slots, workspace, status=
     top-k indices; negative: dropped).  Writes offsets (int32, num_experts + 1), rows
     (int32, tokens * top_k) and slots (int32, tokens x top_k).  workspace:
     MOE_SORT_WORKSPACE_BYTES device bytes."""
-    wide = experts.dtype is torch.int64
-    ep, T, K, stride = _matrix(experts, "experts", torch.int64 if wide else torch.int32)
+    ep, T, K, stride, id_bytes = _matrix(experts, "experts", _IDS)
     if not workspace.is_contiguous():
         raise ValueError("workspace is contiguous")
+    n = T * K
     _enqueue(_lib.zipccl_moe_sort, (experts, offsets, rows, slots, workspace), status, stream,
-             (ep, 8 if wide else 4, stride, T, K, num_experts,
-              _vector(offsets, num_experts + 1, torch.int32, "offsets"), _vector(rows, T * K, torch.int32, "rows"),
-              _vector(slots, T * K, torch.int32, "slots"), workspace.data_ptr(), workspace.nbytes))
+             (ep, id_bytes, stride, T, K, num_experts,
+              _vector(offsets, num_experts + 1, torch.int32, "offsets"), _vector(rows, n, torch.int32, "rows"),
+              _vector(slots, n, torch.int32, "slots"), workspace.data_ptr(), workspace.nbytes))
 
 
 def moe_dispatch(x, slots, y, status=None, stream=None):
     """zipccl_moe_dispatch: y[slots[t, k]] = x[t]."""
-    xp, T, H, xs = _matrix(x, "x")
-    yp, M, yh, ys = _matrix(y, "y", x.dtype)
-    if H != yh:
-        _differ(H, yh, "the rows of x and y")
+    xp, T, H, xs, kind = _matrix(x, "x")
+    yp, M, yh, ys, y_kind = _matrix(y, "y")
+    if H != yh or kind != y_kind:
+        _differ((H, x.dtype), (yh, y.dtype), "the rows of x and y")
     sp, K = _slots(slots, T)
     _enqueue(_lib.zipccl_moe_dispatch, (x, slots, y), status, stream,
-             (xp, xs, sp, T, K, H, _DTYPES[x.dtype], yp, M, ys))
+             (xp, xs, sp, T, K, H, kind, yp, M, ys))
 
 
 def moe_dispatch_backward(dy, slots, dx, status=None, stream=None):
     """zipccl_moe_dispatch_backward: dx[t] = sum over k of dy[slots[t, k]]."""
-    yp, M, H, ys = _matrix(dy, "dy")
-    xp, T, xh, xs = _matrix(dx, "dx", dy.dtype)
-    if H != xh:
-        _differ(H, xh, "the rows of dy and dx")
+    yp, M, H, ys, kind = _matrix(dy, "dy")
+    xp, T, xh, xs, x_kind = _matrix(dx, "dx")
+    if H != xh or kind != x_kind:
+        _differ((H, dy.dtype), (xh, dx.dtype), "the rows of dy and dx")
     sp, K = _slots(slots, T)
     _enqueue(_lib.zipccl_moe_dispatch_backward, (dy, slots, dx), status, stream,
-             (yp, M, ys, sp, T, K, H, _DTYPES[dy.dtype], xp, xs))
+             (yp, M, ys, sp, T, K, H, kind, xp, xs))
 
 
 def moe_combine(y, slots, weights, out, status=None, stream=None):
     """zipccl_moe_combine: out[t] = sum over k of weights[t, k] * y[slots[t, k]] (weights
     float32, or None for 1)."""
-    yp, M, H, ys = _matrix(y, "y")
-    op, T, oh, os_ = _matrix(out, "out", y.dtype)
-    if H != oh:
-        _differ(H, oh, "the rows of y and out")
+    yp, M, H, ys, kind = _matrix(y, "y")
+    op, T, oh, os_, o_kind = _matrix(out, "out")
+    if H != oh or kind != o_kind:
+        _differ((H, y.dtype), (oh, out.dtype), "the rows of y and out")
     sp, K = _slots(slots, T)
     wp = None if weights is None else _vector(weights, T * K, torch.float32, "weights")
-    _enqueue(_lib.zipccl_moe_combine, (y, slots, weights, out), status, stream,
-             (yp, M, ys, sp, wp, T, K, H, _DTYPES[y.dtype], op, os_))
+    _enqueue(_lib.zipccl_moe_combine, (y, slots, out) if weights is None else (y, slots, weights, out), status, stream,
+             (yp, M, ys, sp, wp, T, K, H, kind, op, os_))
 
 
 def moe_combine_backward(dout, y, slots, weights, dy, dweights, status=None, stream=None):
     """zipccl_moe_combine_backward: dy[slots[t, k]] = weights[t, k] * dout[t] and
     dweights[t, k] = <dout[t], y[slots[t, k]]>."""
-    gp, T, gh, gs = _matrix(dout, "dout")
-    yp, M, H, ys = _matrix(y, "y", dout.dtype)
-    dp, dm, dh, ds = _matrix(dy, "dy", dout.dtype)
-    if H != gh:
-        _differ(H, gh, "the rows of y and dout")
-    if M != dm or H != dh:
-        _differ((M, H), (dm, dh), "y and dy")
+    gp, T, gh, gs, g_kind = _matrix(dout, "dout")
+    yp, M, H, ys, kind = _matrix(y, "y")
+    dp, dm, dh, ds, d_kind = _matrix(dy, "dy")
+    if H != gh or kind != g_kind:
+        _differ((H, y.dtype), (gh, dout.dtype), "the rows of y and dout")
+    if M != dm or H != dh or kind != d_kind:
+        _differ((M, H, y.dtype), (dm, dh, dy.dtype), "y and dy")
     sp, K = _slots(slots, T)
     _enqueue(_lib.zipccl_moe_combine_backward, (dout, y, slots, weights, dy, dweights), status, stream,
-             (gp, gs, yp, M, ys, sp, _vector(weights, T * K, torch.float32, "weights"), T, K, H, _DTYPES[y.dtype],
+             (gp, gs, yp, M, ys, sp, _vector(weights, T * K, torch.float32, "weights"), T, K, H, kind,
               dp, ds, _vector(dweights, T * K, torch.float32, "dweights")))
 
 
@@ -722,14 +727,14 @@ def quantize_rows(x, q, scales, slots=None, status=None, stream=None):
     at least as long as x's rows) with float32 scales, to every slot of a token or, without
     slots, row by row.  q is written up to the next multiple of ROW_PAD: rows of fewer columns
     are taken where they start at a multiple of ROW_PAD in a tensor that goes on that far."""
-    xp, T, H, xs = _matrix(x, "x", torch.bfloat16)
-    qp, M, wide, qs = _matrix(q, "q", torch.int8)
+    xp, T, H, xs, _ = _matrix(x, "x", _BF16_ONLY)
+    qp, M, wide, qs, _ = _matrix(q, "q", _INT8)
     if wide < H:
         raise ValueError("q's rows hold x's rows")
     if wide % ROW_PAD:
         _holds_padding(q, qs, H, "q", True)
     sp, K = (None, 1) if slots is None else _slots(slots, T)
-    _enqueue(_lib.zipccl_quantize_rows, (x, q, scales, slots), status, stream,
+    _enqueue(_lib.zipccl_quantize_rows, (x, q, scales) if slots is None else (x, q, scales, slots), status, stream,
              (xp, xs, T, H, sp, K, qp, M, qs, _vector(scales, M, torch.float32, "scales")))
 
 
@@ -738,8 +743,8 @@ def experts_product(q, scales, w, w_scales, row_len: int, out, offsets=None, sta
     experts x outputs x stride (or outputs x stride for one), w_scales float32, experts x
     outputs; row_len: values of a row without its padding; out: rows x outputs, bfloat16
     or float32; offsets: int32, experts + 1 (None: one expert)."""
-    qp, M, wide, qs = _matrix(q, "q", torch.int8)
-    op, om, on, os_ = _matrix(out, "out")
+    qp, M, wide, qs, _ = _matrix(q, "q", _INT8)
+    op, om, on, os_, kind = _matrix(out, "out")
     shape = w.shape
     if len(shape) not in (2, 3):
         raise ValueError("w is experts x outputs x row stride")
@@ -750,11 +755,13 @@ def experts_product(q, scales, w, w_scales, row_len: int, out, offsets=None, sta
         raise ValueError("row_len is at most the row length of q and w")
     if wide % ROW_PAD:
         _holds_padding(q, qs, row_len, "q", False)
-    _enqueue(_lib.zipccl_experts_product, (q, scales, w, w_scales, offsets, out), status, stream,
+    if offsets is None:
+        tensors, starts = (q, scales, w, w_scales, out), None
+    else:
+        tensors, starts = (q, scales, w, w_scales, offsets, out), _vector(offsets, E + 1, torch.int32, "offsets")
+    _enqueue(_lib.zipccl_experts_product, tensors, status, stream,
              (qp, qs, _vector(scales, M, torch.float32, "scales"), M, _vector(w, 0, torch.int8, "w"), ws,
-              _vector(w_scales, E * N, torch.float32, "w_scales"), E, N, row_len,
-              None if offsets is None else _vector(offsets, E + 1, torch.int32, "offsets"), op, os_,
-              _DTYPES[out.dtype]))
+              _vector(w_scales, E * N, torch.float32, "w_scales"), E, N, row_len, starts, op, os_, kind))
 
 
 # ------------------------------------------------------------------------------------
