@@ -94,3 +94,90 @@ def test_nan_products_are_one_bit_pattern(Z, E, M, N, H):
     want[rows], want[:, columns], want[zero_rows] = True, True, True
     assert bool((out.view(torch.int16)[want] == 0x7FC0).all())
     assert bool(out[~want].isfinite().all())
+
+
+# ------------------------------------------------------------------------------------
+# more work than a grid: the kernels' loops take a second turn
+# ------------------------------------------------------------------------------------
+def parts(n, size):
+    return [slice(a, min(n, a + size)) for a in range(0, n, size)]
+
+
+def test_combine_by_waves_of_more_tokens_than_a_grid(Z):
+    # whole 1 KB parts at aligned addresses, past the Infinity Cache: groups of 4 tokens, 65535 in a grid
+    T, H = 4 * 65535 + 9, 512
+    g = torch.Generator(device="cuda").manual_seed(1)
+    y = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    slots = torch.randperm(T, generator=g, device="cuda").int().view(T, 1)
+    weights = torch.rand(T, 1, generator=g, device="cuda")
+    out = torch.full_like(y, 12345.0)
+    Z.moe_combine(y, slots, weights, out)
+    for s in parts(T, 1 << 17):
+        want = y[slots[s, 0].long()].double() * weights[s].double()
+        assert bool(((out[s].double() - want).abs() <= (BF16_REL + 2.0 ** -23) * want.abs()).all())
+
+
+@pytest.mark.parametrize("T,H", [((1 << 20) + 5, 1025), (4 * (1 << 20) + 7, 264)])
+def test_combine_gradient_of_more_tokens_than_a_grid(Z, T, H):
+    # 2^20 workgroups: of a token each, and of four
+    g = torch.Generator(device="cuda").manual_seed(2)
+    y, dout = (torch.randn(T, H, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    slots = torch.randperm(T, generator=g, device="cuda").int().view(T, 1)
+    weights = torch.rand(T, 1, generator=g, device="cuda")
+    dy, dw = torch.full_like(y, 12345.0), torch.full((T, 1), 12345.0, device="cuda")
+    Z.moe_combine_backward(dout, y, slots, weights, dy, dw)
+    for s in parts(T, 1 << 17):
+        at, d = slots[s, 0].long(), dout[s].double()
+        want = d * weights[s].double()
+        assert bool(((dy[at].double() - want).abs() <= (BF16_REL + 2.0 ** -23) * want.abs()).all())
+        terms = d * y[at].double()
+        assert bool(((dw[s, 0].double() - terms.sum(1)).abs() <= H * 2.0 ** -23 * terms.abs().sum(1)).all())
+
+
+@pytest.mark.parametrize("T,H", [((1 << 20) + 5, 2049), (4 * (1 << 20) + 7, 72)])
+def test_quantize_more_tokens_than_a_grid(Z, T, H):
+    # 2^20 workgroups: of a token each, and of four
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(T, H, generator=g, device="cuda", dtype=torch.bfloat16)
+    x[::1000] = 0
+    q = torch.full((T, -(-H // 128) * 128), 99, dtype=torch.int8, device="cuda")
+    scales = torch.full((T,), 12345.0, device="cuda")
+    Z.quantize_rows(x, q, scales)
+    for s in parts(T, 1 << 17):
+        wide = x[s].double()
+        peak = wide.abs().amax(1, keepdim=True)
+        want = torch.round(127 * wide / torch.where(peak == 0, 1.0, peak))
+        assert torch.equal(q[s, :H].double(), want) and not q[s, H:].any()
+        assert bool(((scales[s].double() - peak[:, 0] / 127).abs() <= 2.0 ** -24 * peak[:, 0] / 127).all())
+
+
+# ------------------------------------------------------------------------------------
+# the torch layer with more rows than kept choices
+# ------------------------------------------------------------------------------------
+@pytest.mark.parametrize("count_first", [True, False])
+def test_layer_with_rows_of_no_choice(count_first):
+    from lossless_bf16_exponent_codec_amd import moe
+    T, K, E, H, rows = 50, 2, 4, 96, 130
+    g = torch.Generator(device="cuda").manual_seed(4)
+    ids = torch.rand(T, E, generator=g, device="cuda").topk(K).indices
+    ids[5], ids[9, 1] = -1, -1
+    routing = moe.route(ids, E)
+    if count_first:
+        assert routing.splits()[-1] == 97
+    x, f, w, dout = (torch.randn(*s, generator=g, device="cuda") for s in ((T, H), (H, H), (T, K), (T, H)))
+    leaves = [t.requires_grad_() for t in (x, f, w)]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    del_me = torch.full((rows, H), float("nan"), device="cuda")   # memory that the layer's buffers may be made of
+    del del_me
+    y = moe.dispatch(x, routing, rows, status)
+    assert not y[97:].any()
+    out = moe.combine(y @ f, routing, w, status)
+    got = torch.autograd.grad(out, leaves, dout)
+    wide = [t.detach().double().cpu().requires_grad_() for t in leaves]
+    kept = (ids >= 0).double().cpu()
+    ref = ((wide[2] * kept).sum(1, keepdim=True)) * (wide[0] @ wide[1])
+    want = torch.autograd.grad(ref, wide, dout.double().cpu())
+    # sums of fewer than 200 terms, two in a row, doubled for the library's products, relative to the largest value
+    for a, b in zip((out.detach(), *got), (ref.detach(), *want)):
+        assert float((a.double().cpu() - b).abs().max()) <= 4 * 200 * 2.0 ** -23 * float(b.abs().max())
+    assert int(status.item()) == 0
