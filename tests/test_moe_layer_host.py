@@ -166,3 +166,15 @@ def test_status_word_of_each_call(moe, monkeypatch):
     experts = moe.QuantizedExperts(torch.zeros(3, 5, 250, dtype=torch.bfloat16))
     experts(moe.QuantizedRows(torch.zeros(4, 256, dtype=torch.int8), torch.zeros(4), 250), routing, status=status)
     assert int(status) == 64
+
+
+def test_weights_of_other_choices_are_refused(moe):
+    # a weight for each choice; more would be read at the wrong places, and their gradients
+    # would be memory as it was found
+    routing = moe.route(IDS, 3)
+    rows = torch.randn(5, 4)
+    want = moe.combine(rows, routing, torch.arange(6.0).view(3, 2))
+    assert torch.equal(moe.combine(rows, routing, torch.arange(6.0)), want)
+    for shape in (3, 3), (2, 3), (4, 2), (7,), (3, 1), (5,):
+        with pytest.raises(ValueError, match="weights"):
+            moe.combine(rows, routing, torch.ones(shape))
