@@ -29,14 +29,15 @@ def dispatch(x, slots, y, status=None):
 
 
 def combine(y, slots, weights, out, status=None):
-    w = torch.ones(slots.shape) if weights is None else weights
+    w = torch.ones(slots.shape) if weights is None else weights.reshape(slots.shape)
     out.copy_((w.unsqueeze(-1) * picked(y, slots)).sum(1))
     if status is not None and bool((slots >= y.shape[0]).any()):
         status |= 4
 
 
 def combine_backward(dout, y, slots, weights, dy, dweights, status=None):
-    dweights.copy_((dout.unsqueeze(1) * picked(y, slots)).sum(-1))
+    weights = weights.reshape(slots.shape)
+    dweights.copy_((dout.unsqueeze(1) * picked(y, slots)).sum(-1).view(dweights.shape))
     for t, k in (slots >= 0).nonzero().tolist():
         if slots[t, k] < y.shape[0]:
             dy[slots[t, k]] = weights[t, k] * dout[t]
