@@ -535,11 +535,12 @@ __device__ inline void product_tile(const ProductArgs& a, uint8_t* s_ring, uint3
         __builtin_amdgcn_wave_barrier();
     }
 
+    if (a.fp32) return;
     // the lanes of a wave hold the scales of all its rows and outputs
     bool plain = to.finite();
 #pragma unroll
     for (uint32_t i = 0; i < kM; i++) plain &= tame(scale[i]);
-    if (__all(plain) || a.fp32) return;
+    if (__all(plain)) return;
 #pragma unroll 1
     for (uint32_t at = wm + lane / kPerRow; at < min(wm + 32 * kM, rows); at += 64 / kPerRow) to.one_nan(a, row0 + at);
 }
@@ -707,7 +708,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void product_split_kernel(const Pr
             hi += at[1];
         }
         to.store(a, row0 + out_row, __builtin_convertvector(lo, v4f) * scale, __builtin_convertvector(hi, v4f) * scale);
-        if (!(to.finite() && tame(scale)) && !a.fp32) to.one_nan(a, row0 + out_row);
+        if (!a.fp32 && !(to.finite() && tame(scale))) to.one_nan(a, row0 + out_row);
     }
 }
 
