@@ -36,9 +36,10 @@ __device__ inline void set_status(uint32_t* status, uint32_t bits)
 // Nothing here is bound by bandwidth (2 MB for 131072 choices); what counts is the chain
 // of dependent steps.  A wave therefore ranks its choices once, holds the ranks in
 // registers across the scan over experts, and adds the expert's base after it.  Over 256
-// experts 512 choices take 3.4 us (one launch, near the shortest one), 131072 take 9.0:
-// 2.9 to count, the rest to place, which reads the other workgroups' counts (8 16-byte loads
-// in flight per thread; 16 of 4 bytes took 0.8 us more, one after another 3 more still).
+// experts 512 choices take 3.4 us (one launch, near the shortest one).  131072 take 9.0 in a
+// row of calls; traced one by one, the count takes 2.8 to 3.0 and the placing 7.0 to 7.2,
+// which reads the other workgroups' counts (8 16-byte loads in flight per thread; 16 of 4
+// bytes took 0.8 us more, one after another 3 more still).
 // ------------------------------------------------------------------------------------
 __device__ inline int32_t load_id(const SortArgs& a, uint32_t i, bool& bad)
 {
@@ -255,11 +256,11 @@ template <> struct Raw<16> { typedef uint4 type; };
 template <> struct Raw<4> { typedef uint32_t type; };
 template <> struct Raw<2> { typedef uint16_t type; };
 
-// kStream: non-temporal accesses, for rows that do not fit the Infinity Cache (16384 tokens
-// of 7168 to 8 rows each, 1.9 GB: dispatch 346 us, 385 with plain stores; combine 345 us,
-// 400 with plain loads, the tokens in the cache).  What fits is left to the caches (4096 tokens of 4098 to 4 rows
-// each, 168 MB: dispatch 26.4 us, 36.4 with non-temporal stores, whose lines at the ends of
-// rows are written in parts; combine 25.1 and 30.6).
+// kStream: non-temporal accesses, for rows that do not fit the Infinity Cache (combine of 16384
+// tokens of 7168 from 8 rows each, 1.9 GB: 345 us, 400 with plain loads; the dispatch's stores
+// by shared waves are within 3 % either way, 370 and 366).  What fits is left to the caches
+// (4096 tokens of 4098 to 4 rows each, 168 MB: dispatch 26.4 us, 36.4 with non-temporal
+// stores, whose lines at the ends of rows are written in parts; combine 25.1 and 30.6).
 typedef uint32_t Quad __attribute__((ext_vector_type(4), aligned(2)));
 
 template <uint32_t BYTES, bool kStream>
@@ -333,7 +334,7 @@ struct Chunk {
 
 struct RowShape {
     uint32_t bytes;    // of a row
-    uint32_t chunks;   // of `unit` bytes, the last one overlapping where bytes is no multiple
+    uint32_t chunks;   // the last one overlapping where bytes is no multiple of a chunk's
 
     template <uint32_t BYTES>
     __device__ inline uint32_t at(uint32_t c) const   // byte offset of chunk c
@@ -459,9 +460,14 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(const RowsArgs a)
 
 // Dispatch by waves, for rows that stream: kShare waves load the same 1 KB of a token (one
 // of them from memory) and write it to every kShare-th of its slots, kParts neighbouring KB
-// per workgroup.  16384 tokens of 7168 from HBM to 8 rows each: 351 us, 417 where one wave
-// wrote all 8 rows (4 waves, 1 KB per workgroup 368; 2 waves, 2 KB 374; 1 wave, 4 KB 384).
-// Two rows per wave are best: at 4 rows 2 waves take 203 us, 4 take 243, 1 takes 217.
+// per workgroup.  16384 tokens of 7168 from HBM to 8 rows of 64 skewed experts: 351 us, 417
+// where one wave wrote all 8 rows (4 waves, 1 KB per workgroup 368; 2 waves, 2 KB 374; 1 wave, 4 KB
+// 384).  One, two and four waves, to rows of 64 evenly chosen experts, in us:
+//   1 row    83   82  130     5 rows  257  244  278     10 rows  477  487  477
+//   2 rows  131  125  198     6 rows  301  301  309     12 rows  564  575  576
+//   3 rows  170  156  217     7 rows  344  343  332     16 rows  748  755  758
+//   4 rows  214  211  240     8 rows  388  397  370     64 rows (4096 tokens)  703  695  679
+// so two waves below 7 rows and four from there on, 2 % off at 12 and 16 rows.
 constexpr uint32_t kParts = 4;
 
 template <uint32_t kShare>
