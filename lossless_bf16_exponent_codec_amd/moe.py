@@ -99,8 +99,9 @@ def dispatch(x: torch.Tensor, routing: Routing, nrows: int, status=None) -> torc
 def combine(y: torch.Tensor, routing: Routing, weights: torch.Tensor, status=None) -> torch.Tensor:
     """Tokens from rows by expert: sums with weights (float32, tokens x top_k);
     differentiable in y and weights."""
-    if weights.numel() != routing.slots.numel() or (weights.dim() == 2 and weights.shape != routing.slots.shape):
-        raise ValueError(f"weights are {tuple(weights.shape)}, choices are {tuple(routing.slots.shape)}")
+    shape, choices = weights.shape, routing.slots.shape   # or any shape with the same order
+    if shape.numel() != choices.numel() or (len(shape) == 2 and shape != choices and 1 not in shape):
+        raise ValueError(f"weights are {tuple(shape)}, choices are {tuple(choices)}")
     return _Combine.apply(y, routing.slots, weights.contiguous(), status)
 
 

@@ -640,8 +640,8 @@ def _one_device(tensors) -> int:
 
 def _enqueue_on(device, call, status, stream, args):
     if status is not None and not isinstance(status, int):
-        if status.nbytes < 4 or not status.is_contiguous():
-            raise ValueError("status is a contiguous tensor of at least 4 bytes")
+        if status.nbytes < 4 or (status.element_size() < 4 and not status.is_contiguous()):
+            raise ValueError("status is a tensor whose first 4 bytes are its own")
         other = status.get_device()
         if other != device and _one_device([status]) != device:
             _differ(other, device, "the GPUs of status and the other tensors")

@@ -178,7 +178,12 @@ def test_workspace_and_status_hold_what_is_written(Z):
                 torch.zeros(1, dtype=torch.uint8).expand(4):
             with pytest.raises(ValueError, match="status"):
                 call(Z, tensors, status=placed(status))
-    assert not Z.calls
+        assert not Z.calls
+        for status in torch.zeros(1, dtype=torch.int64), torch.zeros(4, dtype=torch.uint8), \
+                torch.zeros(4, 4, dtype=torch.int32)[:, 1]:
+            call(Z, tensors, status=placed(status))
+        assert len(Z.calls) == 3
+        Z.calls.clear()
 
 
 def test_strides_whose_last_row_has_no_64_bit_address_are_refused():

@@ -175,7 +175,8 @@ def test_weights_of_other_choices_are_refused(moe):
     routing = moe.route(IDS, 3)
     rows = torch.randn(5, 4)
     want = moe.combine(rows, routing, torch.arange(6.0).view(3, 2))
-    assert torch.equal(moe.combine(rows, routing, torch.arange(6.0)), want)
+    for shape in (6,), (6, 1), (1, 6), (3, 2, 1):
+        assert torch.equal(moe.combine(rows, routing, torch.arange(6.0).view(shape)), want)
     for shape in (3, 3), (2, 3), (4, 2), (7,), (3, 1), (5,):
         with pytest.raises(ValueError, match="weights"):
             moe.combine(rows, routing, torch.ones(shape))
