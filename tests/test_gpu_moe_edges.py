@@ -154,9 +154,10 @@ def test_quantize_more_tokens_than_a_grid(Z, T, H):
 # ------------------------------------------------------------------------------------
 # the torch layer with more rows than kept choices
 # ------------------------------------------------------------------------------------
-@pytest.mark.parametrize("count_first", [True, False])
-def test_layer_with_rows_of_no_choice(count_first):
+@pytest.mark.parametrize("count_first,apart", [(True, 0), (False, 0), (False, 1 << 40)])
+def test_layer_with_rows_of_no_choice(count_first, apart, monkeypatch):
     from lossless_bf16_exponent_codec_amd import moe
+    monkeypatch.setattr(moe, "CLEAR_APART", apart)
     T, K, E, H, rows = 50, 2, 4, 96, 130
     g = torch.Generator(device="cuda").manual_seed(4)
     ids = torch.rand(T, E, generator=g, device="cuda").topk(K).indices

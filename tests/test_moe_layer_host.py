@@ -119,12 +119,14 @@ def poison():
     torch.use_deterministic_algorithms(False)
 
 
-def test_rows_of_no_choice_are_zero(moe, poison):
+@pytest.mark.parametrize("apart", [0, 1 << 40])
+def test_rows_of_no_choice_are_zero(moe, poison, monkeypatch, apart):
     # 5 kept choices in a buffer of 8 rows, with the kept count on the host and without: the
     # rows past them are read by a dense expert and by its weights' gradient
     g = torch.Generator().manual_seed(3)
     x, f = torch.randn(3, 4, generator=g), torch.randn(4, 4, generator=g)
     assert bool(torch.empty(3).isnan().all())
+    monkeypatch.setattr(moe, "CLEAR_APART", apart)
     for count_first in True, False:
         routing = moe.route(IDS, 3)
         if count_first:
