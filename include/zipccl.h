@@ -496,6 +496,114 @@ zipccl_status zipccl_experts_product(const void* q, uint64_t q_stride, const flo
                                      uint64_t outputs, uint64_t row_len, const int32_t* offsets, void* out,
                                      uint64_t out_stride, int out_dtype, uint32_t* status, void* stream);
 
+/* ---- The router of a mixture-of-experts layer ----
+ * From a token's logits z (one per expert, dtype ZIPCCL_BF16 or ZIPCCL_FP32, row stride in
+ * values, any alignment of one value):
+ *   choices   the top_k experts with the largest logits, in descending order, the lowest
+ *             number first among equals.  An expert whose logit is minus infinity is closed:
+ *             it is never chosen.  A NaN ranks above every number.  A token with fewer open
+ *             experts than top_k has -1 (dropped) in the places left, with weight 0.
+ *   weights   with p = softmax(z): p[choice], or p[choice] / sum of p over the choices
+ *             (renormalize != 0).  A NaN or plus infinity among the logits makes them NaN.
+ *   balance   over the n tokens that count, with counts[e] choices of expert e and
+ *             sums[e] = sum over the tokens of p[e]:
+ *             loss = num_experts / (top_k * n * n) * sum over e of counts[e] * sums[e]
+ *             (1 for an even spread; 0 if n is 0)
+ * mask (device uint8[tokens], or NULL) holds 0 for a token that takes no part (padding): its
+ * logits, which may be anything, and choices are not looked at, it gets choices of -1 and
+ * weights of 0, is not counted, and its gradient is 0.  A token all of whose experts are closed
+ * is treated alike.
+ * Sums over tokens are fp32 within a workgroup and fp64 over those, in a fixed order: every
+ * result is the same on every run. */
+#define ZIPCCL_MOE_GATE_WORKSPACE_BYTES (256u * (8u * ZIPCCL_MAX_EXPERTS + 16u))
+
+/* Choices and weights, and, where counts is not NULL, the balance outputs.
+ *   experts   device int32[tokens * top_k] (what zipccl_moe_sort takes); weights: device
+ *             fp32[tokens * top_k]
+ *   counts    device int32[num_experts + 1], or NULL: the last one is n.  sums: device
+ *             fp32[num_experts], loss: device fp32[1]; both NULL where counts is.  counts and
+ *             sums of several ranks may be added: the loss of all their tokens, and with the
+ *             added counts zipccl_moe_gate_backward's gradient of it, follow from them.
+ *   workspace device scratch, 256-byte aligned, ZIPCCL_MOE_GATE_WORKSPACE_BYTES, or NULL
+ *             where counts is; carries nothing between calls; concurrent calls need separate
+ *             ones
+ * One launch, two with the balance outputs.
+ * Errors: INVALID (NULL pointers, dtype, num_experts outside 1..ZIPCCL_MAX_EXPERTS, top_k
+ * outside 1..ZIPCCL_MAX_TOP_K or above num_experts, stride < num_experts), ALIGN, SIZE, HIP. */
+zipccl_status zipccl_moe_gate(const void* logits, int dtype, uint64_t stride, uint64_t tokens, int num_experts,
+                              const uint8_t* mask, int top_k, int renormalize, int32_t* experts, float* weights,
+                              int32_t* counts, float* sums, float* loss, void* workspace, uint64_t workspace_bytes,
+                              uint32_t* status, void* stream);
+
+/* The balance outputs for choices that the caller made: experts as in zipccl_moe_sort
+ * (int32 or int64, row stride id_stride; negative: dropped; >= num_experts: dropped, with
+ * ZIPCCL_STATUS_BAD_INDEX).  An expert named twice by a token counts twice.  top_k may be above
+ * num_experts.  Errors: as zipccl_moe_gate (and id_bytes, id_stride < top_k: INVALID). */
+zipccl_status zipccl_moe_balance(const void* logits, int dtype, uint64_t stride, uint64_t tokens, int num_experts,
+                                 const uint8_t* mask, const void* experts, int id_bytes, uint64_t id_stride, int top_k,
+                                 int32_t* counts, float* sums, float* loss, void* workspace, uint64_t workspace_bytes,
+                                 uint32_t* status, void* stream);
+
+/* Gradient by the logits, dlogits (tokens x num_experts, of their dtype), for gradients of
+ *   the weights   dweights: device fp32[tokens * top_k], or NULL: none.  A dropped choice's is
+ *                 not read into a sum.  Choices of a token that are all closed have weights,
+ *                 and so gradients, of 0.
+ *   the loss      dloss: device fp32[1], with counts as the forward call wrote them; both
+ *                 NULL: none
+ * The choices (as in zipccl_moe_balance; those of the forward pass) are constants; those that
+ * a token names twice add up.  One launch.
+ * Errors: as zipccl_moe_balance; INVALID also where neither gradient is given, and where one
+ * of dloss and counts is NULL alone. */
+zipccl_status zipccl_moe_gate_backward(const void* logits, int dtype, uint64_t stride, uint64_t tokens,
+                                       int num_experts, const uint8_t* mask, const void* experts, int id_bytes,
+                                       uint64_t id_stride, int top_k, int renormalize, const float* dweights,
+                                       const int32_t* counts, const float* dloss, void* dlogits, uint64_t dlogits_stride,
+                                       uint32_t* status, void* stream);
+
+/* ---- Experts' weights in 4 bits ----
+ * q[e][n][h], whole numbers from -8 to 7, with a scale for each output n and group of inputs h
+ * (group: 32, 64 or a multiple of 128).
+ *   weights   bytes, for each expert ceil(outputs / 16) x ceil(row_len / 128) tiles of 1024
+ *             bytes, the tiles of 16 outputs one after another along the inputs.  In a tile of
+ *             outputs 16 a + o and inputs 128 b + 32 i + 8 g + j (o < 16; i, g < 4; j < 8) the
+ *             little-endian dword 4 * (16 g + o) + i holds q as two's complement in bits 4 j ..
+ *             4 j + 3.  Places past outputs or row_len hold 0.
+ *   scales    num_experts x ceil(row_len / group) x outputs, BF16 or FP32 (scale_dtype) */
+#define ZIPCCL_TILE4_OUTPUTS 16
+#define ZIPCCL_TILE4_INPUTS 128
+#define ZIPCCL_TILE4_BYTES 1024
+
+/* Bytes of the weights of num_experts experts. */
+uint64_t zipccl_weights4_size(int num_experts, uint64_t outputs, uint64_t row_len);
+
+/* BF16 weights w (num_experts * outputs rows) in 4 bits: a group's scale is s = max |w| / 7
+ * rounded to scale_dtype, q = rint(w / s) in fp32, within -8 .. 7 (s = 0: q = 0; a group with a
+ * NaN or an infinity: q = 0 and scale NaN).  q: device, 16-byte aligned.
+ * Errors: INVALID (NULL pointers, group, scale_dtype, sizes of 0, num_experts, w_stride <
+ * row_len), ALIGN, SIZE, HIP. */
+zipccl_status zipccl_quantize_weights4(const void* w, uint64_t w_stride, int num_experts, uint64_t outputs,
+                                       uint64_t row_len, uint64_t group, void* q, void* scales, int scale_dtype,
+                                       void* stream);
+
+/* The experts' product with 4-bit weights: for the rows s of expert e (offsets[e] <= s <
+ * offsets[e + 1]) and n < outputs
+ *   out[s][n] = sum over h of x[index[s]][h] * q[e][n][h] * scale[e][h / group][n]
+ * with fp32 sums in a fixed order, rounded once to out_dtype (a NaN in BF16 is 0x7FC0).
+ *   x         device, x_rows rows of row_len BF16 values
+ *   index     device int32[rows], as zipccl_moe_sort's rows: the row of x (a token) of each
+ *             row; one outside 0..x_rows-1 in an expert's range sets ZIPCCL_STATUS_BAD_INDEX and
+ *             counts as a row of zeros.  NULL: row s of x, and rows = x_rows.
+ *   offsets   as in zipccl_experts_product (rows outside every expert's range are left as they
+ *             were)
+ *   q, scales as above; q is 16-byte aligned
+ * Errors: INVALID, ALIGN, SIZE (row_len > 2^24, outputs >= 2^24, rows * outputs beyond one
+ * launch), HIP. */
+zipccl_status zipccl_experts_product4(const void* x, uint64_t x_stride, uint64_t x_rows, const int32_t* index,
+                                      uint64_t rows, const void* q, const void* scales, int scale_dtype,
+                                      uint64_t group, int num_experts, uint64_t outputs, uint64_t row_len,
+                                      const int32_t* offsets, void* out, uint64_t out_stride, int out_dtype,
+                                      uint32_t* status, void* stream);
+
 /* Static text for a status code. */
 const char* zipccl_strerror(zipccl_status s);
 

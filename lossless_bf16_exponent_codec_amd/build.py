@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libzipccl.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("zipccl_kernels.hip", "zipccl_host.cpp", "zipccl_moe.hip",
-                                           "zipccl_experts.hip", "zipccl_moe_host.cpp")]
+                                           "zipccl_experts.hip", "zipccl_gate.hip", "zipccl_experts4.hip",
+                                           "zipccl_moe_host.cpp")]
 PROBE_LIB = os.path.join(PKG, "libzcprobe.so")
 PROBE_SOURCES = [os.path.join(CSRC, "stream_probe.hip")]
 ARCH = "gfx950"

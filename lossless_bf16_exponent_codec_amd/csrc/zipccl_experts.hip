@@ -14,6 +14,7 @@
 
 #include "zipccl.h"
 #include "zipccl_moe_internal.h"
+#include "zipccl_row_tiles.h"
 
 namespace zc {
 
@@ -22,21 +23,6 @@ namespace {
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v16i __attribute__((ext_vector_type(16)));
 typedef float v4f __attribute__((ext_vector_type(4)));
-
-__device__ inline uint32_t lane_id() { return __lane_id(); }
-
-__device__ inline void set_status(uint32_t* status, uint32_t bits)
-{
-    if (status) atomicOr(status, bits);
-}
-
-// Two values rounded to BF16 (to nearest even; a NaN keeps its sign and payload).
-__device__ inline uint32_t bf16_pair(float lo, float hi)
-{
-    typedef float f2 __attribute__((ext_vector_type(2)));
-    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{lo, hi}), b2));
-}
 
 // ------------------------------------------------------------------------------------
 // Quantisation of rows
@@ -195,76 +181,6 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_rows_kernel(const Quan
 // ------------------------------------------------------------------------------------
 // Experts' product
 // ------------------------------------------------------------------------------------
-
-// The rows [begin, end) of an expert, from offsets that are kept in range whatever the
-// caller's hold.
-__device__ inline void expert_rows(const ProductArgs& a, uint32_t e, uint32_t& begin, uint32_t& end)
-{
-    if (!a.offsets) {
-        begin = 0;
-        end = a.rows;
-        return;
-    }
-    const int64_t lo = a.offsets[e], hi = a.offsets[e + 1];
-    if (lo < 0 || hi < lo || hi > int64_t(a.rows)) set_status(a.status, ZIPCCL_STATUS_BAD_INDEX);
-    begin = uint32_t(min(max(lo, int64_t(0)), int64_t(a.rows)));
-    end = uint32_t(min(max(hi, int64_t(begin)), int64_t(a.rows)));
-}
-
-// Row tiles of kRows rows, counted expert after expert.  Every wave works them out for
-// itself from the offsets: lane l looks at experts l, 64 + l, ...
-template <uint32_t kRows>
-struct RowTiles {
-    uint32_t begin, end, tiles, sum;   // of expert `lane` of the 64 at hand; sum: running, over lanes
-
-    __device__ inline void look(const ProductArgs& a, uint32_t e0)
-    {
-        begin = end = 0;
-        if (e0 + lane_id() < a.experts) expert_rows(a, e0 + lane_id(), begin, end);
-        sum = tiles = (end - begin + kRows - 1) / kRows;
-        for (uint32_t d = 1; d < 64; d <<= 1) {
-            const uint32_t up = __shfl_up(sum, d);
-            if (lane_id() >= d) sum += up;
-        }
-    }
-
-    __device__ inline RowTiles(const ProductArgs& a) { look(a, 0); }
-
-    __device__ inline uint32_t here() const { return __builtin_amdgcn_readlane(sum, 63); }
-
-    // Tiles of all experts.
-    __device__ inline uint32_t count(const ProductArgs& a)
-    {
-        uint32_t n = here();
-        for (uint32_t e0 = 64; e0 < a.experts; e0 += 64) {
-            look(a, e0);
-            n += here();
-        }
-        if (a.experts > 64) look(a, 0);
-        return n;
-    }
-
-    // Expert and rows of tile `tile`; false past the last.
-    __device__ inline bool find(const ProductArgs& a, uint32_t tile, uint32_t& expert, uint32_t& row0, uint32_t& rows)
-    {
-        uint32_t before = 0;
-        for (uint32_t e0 = 0;;) {
-            const uint64_t past = __ballot(before + sum > tile);
-            if (past) {
-                const uint32_t l = uint32_t(__builtin_ctzll(past));
-                const uint32_t at = tile - before - (__builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(tiles, l));
-                expert = e0 + l;
-                row0 = __builtin_amdgcn_readlane(begin, l) + at * kRows;
-                rows = min(kRows, __builtin_amdgcn_readlane(end, l) - row0);
-                return true;
-            }
-            before += here();
-            e0 += 64;
-            if (e0 >= a.experts) return false;
-            look(a, e0);
-        }
-    }
-};
 
 // Whether sums times a row's scale are finite: no product of 31 bits and a scale below 2^96
 // is infinite.
@@ -568,7 +484,7 @@ template <uint32_t kM, uint32_t kN, uint32_t kSlots, uint32_t kPerCu>
 __global__ __launch_bounds__(kTileThreads, kPerCu) void product_tile_kernel(const ProductArgs a)
 {
     extern __shared__ __attribute__((aligned(1024))) uint8_t s_ring[];
-    RowTiles<64 * kM> map(a);
+    RowTiles<64 * kM, ProductArgs> map(a);
     const uint32_t across = (a.outputs + 64 * kN - 1) / (64 * kN), down = map.count(a);
     const uint32_t t = run_of_xcd(blockIdx.x, down * across);
     if (t >= down * across) return;
@@ -587,7 +503,7 @@ constexpr uint32_t kCus = 256, kCutTiles = kCus / 2;
 __global__ __launch_bounds__(kTileThreads, 1) void product_large_kernel(const ProductArgs a)
 {
     extern __shared__ __attribute__((aligned(1024))) uint8_t s_ring[];
-    RowTiles<256> map(a);
+    RowTiles<256, ProductArgs> map(a);
     const uint32_t across = (a.outputs + 255) / 256, down = map.count(a), total = down * across;
     const uint32_t left = total % kCus;
     const uint32_t whole = left <= kCutTiles ? total - left : total;   // the tiles not cut
@@ -623,7 +539,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void product_split_kernel(const Pr
     extern __shared__ __attribute__((aligned(1024))) uint8_t s_ring[];
     const uint32_t across = (a.outputs + kSplitOuts - 1) / kSplitOuts;
     uint32_t expert, row0, rows;
-    RowTiles<64> map(a);
+    RowTiles<64, ProductArgs> map(a);
     if (a.experts > 64 && blockIdx.x == 0) map.count(a);   // one workgroup looks at every offset, for the status
     if (!map.find(a, blockIdx.x / across, expert, row0, rows)) return;
     const uint32_t n0 = blockIdx.x % across * kSplitOuts;
@@ -710,13 +626,6 @@ __global__ __launch_bounds__(kTileThreads, 1) void product_split_kernel(const Pr
         to.store(a, row0 + out_row, __builtin_convertvector(lo, v4f) * scale, __builtin_convertvector(hi, v4f) * scale);
         if (!a.fp32 && !(to.finite() && tame(scale))) to.one_nan(a, row0 + out_row);
     }
-}
-
-// Row tiles that any split of `rows` rows over the experts can need.
-uint64_t most_tiles(const ProductArgs& a, uint32_t per_tile)
-{
-    const uint64_t parts = a.experts < a.rows ? a.experts : a.rows;
-    return (a.rows + parts * (per_tile - 1)) / per_tile;
 }
 
 }  // namespace

@@ -11,7 +11,9 @@ using namespace zc;
 namespace {
 
 static_assert(ZIPCCL_MAX_EXPERTS == kMaxExperts && ZIPCCL_MAX_TOP_K == kMaxTopK && ZIPCCL_ROW_PAD == kQuantPad &&
-              ZIPCCL_MOE_SORT_WORKSPACE_BYTES == kSortWorkspace, "the header states the limits");
+              ZIPCCL_MOE_SORT_WORKSPACE_BYTES == kSortWorkspace && ZIPCCL_MOE_GATE_WORKSPACE_BYTES == kGateWorkspace &&
+              ZIPCCL_TILE4_OUTPUTS == kTile4 && ZIPCCL_TILE4_INPUTS == kSlab4 && ZIPCCL_TILE4_BYTES == kTileBytes4,
+              "the header states the limits");
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -69,6 +71,55 @@ void split_choices(SortArgs& a)
     a.blocks = uint32_t((a.n + uint64_t(a.per_block) - 1) / a.per_block);
     if (a.blocks == 0) a.blocks = 1;
 }
+
+// The logits' side of the router's calls.
+zipccl_status check_logits(const void* logits, int dtype, uint64_t stride, uint64_t tokens, int num_experts,
+                           int top_k, const uint32_t* status)
+{
+    if (!is_dtype(dtype) || num_experts < 1 || num_experts > kMaxExperts || top_k < 1 || top_k > kMaxTopK)
+        return ZIPCCL_ERR_INVALID;
+    if (tokens >= kMaxCount || tokens * uint64_t(top_k) >= kMaxCount) return ZIPCCL_ERR_SIZE;
+    if (status && !aligned(status, 4)) return ZIPCCL_ERR_ALIGN;
+    return check_rows(logits, tokens, uint64_t(num_experts), stride, dtype);
+}
+
+zipccl_status check_choices(const void* experts, int id_bytes, uint64_t id_stride, uint64_t tokens, int top_k)
+{
+    if (id_bytes != 4 && id_bytes != 8) return ZIPCCL_ERR_INVALID;
+    if (tokens > 0 && !experts) return ZIPCCL_ERR_INVALID;
+    if (tokens > 1 && id_stride < uint64_t(top_k)) return ZIPCCL_ERR_INVALID;
+    if (too_far(tokens, id_stride)) return ZIPCCL_ERR_SIZE;
+    return aligned(experts, uintptr_t(id_bytes)) ? ZIPCCL_OK : ZIPCCL_ERR_ALIGN;
+}
+
+zipccl_status check_balance(const int32_t* counts, const float* sums, const float* loss, const void* workspace,
+                            uint64_t workspace_bytes)
+{
+    if (!counts || !sums || !loss || !workspace) return ZIPCCL_ERR_INVALID;
+    if (workspace_bytes < kGateWorkspace) return ZIPCCL_ERR_SIZE;
+    return aligned(counts, 4) && aligned(sums, 4) && aligned(loss, 4) && aligned(workspace, 256) ? ZIPCCL_OK
+                                                                                              : ZIPCCL_ERR_ALIGN;
+}
+
+GateArgs gate_args(const void* logits, int dtype, uint64_t stride, uint64_t tokens, int num_experts,
+                   const uint8_t* mask, int top_k, uint32_t* status)
+{
+    GateArgs a{};
+    a.logits = static_cast<const uint8_t*>(logits);
+    a.mask = mask;
+    a.status = status;
+    a.stride = stride;
+    a.tokens = tokens;
+    a.num_experts = uint32_t(num_experts);
+    a.top_k = uint32_t(top_k);
+    a.fp32 = dtype == ZIPCCL_FP32;
+    return a;
+}
+
+bool is_group(uint64_t group) { return group == 32 || group == 64 || (group > 0 && group % kSlab4 == 0); }
+
+constexpr uint64_t kMaxOutputs = 1ull << 24;
+constexpr uint64_t kMaxRowLen4 = 1ull << 24;
 
 }  // namespace
 
@@ -263,6 +314,146 @@ zipccl_status zipccl_experts_product(const void* q, uint64_t q_stride, const flo
     a.fp32 = out_dtype == ZIPCCL_FP32;
     if (product_workgroups(a) >= kMaxTiles) return ZIPCCL_ERR_SIZE;
     return hip_status(launch_experts_product(a, static_cast<hipStream_t>(stream)));
+}
+
+zipccl_status zipccl_moe_gate(const void* logits, int dtype, uint64_t stride, uint64_t tokens, int num_experts,
+                              const uint8_t* mask, int top_k, int renormalize, int32_t* experts, float* weights,
+                              int32_t* counts, float* sums, float* loss, void* workspace, uint64_t workspace_bytes,
+                              uint32_t* status, void* stream)
+{
+    if (zipccl_status r = check_logits(logits, dtype, stride, tokens, num_experts, top_k, status)) return r;
+    if (top_k > num_experts || (tokens > 0 && (!experts || !weights))) return ZIPCCL_ERR_INVALID;
+    if (!aligned(experts, 4) || !aligned(weights, 4)) return ZIPCCL_ERR_ALIGN;
+    if (counts) {
+        if (zipccl_status r = check_balance(counts, sums, loss, workspace, workspace_bytes)) return r;
+    } else if (sums || loss) {
+        return ZIPCCL_ERR_INVALID;
+    }
+    GateArgs a = gate_args(logits, dtype, stride, tokens, num_experts, mask, top_k, status);
+    a.renormalize = renormalize != 0;
+    a.experts = experts;
+    a.weights = weights;
+    a.counts = counts;
+    a.sums = sums;
+    a.loss = loss;
+    a.workspace = static_cast<uint8_t*>(workspace);
+    if (tokens == 0 && !counts) return ZIPCCL_OK;
+    return hip_status(launch_moe_gate(a, static_cast<hipStream_t>(stream)));
+}
+
+zipccl_status zipccl_moe_balance(const void* logits, int dtype, uint64_t stride, uint64_t tokens, int num_experts,
+                                 const uint8_t* mask, const void* experts, int id_bytes, uint64_t id_stride, int top_k,
+                                 int32_t* counts, float* sums, float* loss, void* workspace, uint64_t workspace_bytes,
+                                 uint32_t* status, void* stream)
+{
+    if (zipccl_status r = check_logits(logits, dtype, stride, tokens, num_experts, top_k, status)) return r;
+    if (zipccl_status r = check_choices(experts, id_bytes, id_stride, tokens, top_k)) return r;
+    if (zipccl_status r = check_balance(counts, sums, loss, workspace, workspace_bytes)) return r;
+    GateArgs a = gate_args(logits, dtype, stride, tokens, num_experts, mask, top_k, status);
+    a.ids = experts;
+    a.id_stride = id_stride;
+    a.wide_ids = id_bytes == 8;
+    a.counts = counts;
+    a.sums = sums;
+    a.loss = loss;
+    a.workspace = static_cast<uint8_t*>(workspace);
+    return hip_status(launch_moe_gate(a, static_cast<hipStream_t>(stream)));
+}
+
+zipccl_status zipccl_moe_gate_backward(const void* logits, int dtype, uint64_t stride, uint64_t tokens,
+                                       int num_experts, const uint8_t* mask, const void* experts, int id_bytes,
+                                       uint64_t id_stride, int top_k, int renormalize, const float* dweights,
+                                       const int32_t* counts, const float* dloss, void* dlogits, uint64_t dlogits_stride,
+                                       uint32_t* status, void* stream)
+{
+    if (zipccl_status r = check_logits(logits, dtype, stride, tokens, num_experts, top_k, status)) return r;
+    if (zipccl_status r = check_choices(experts, id_bytes, id_stride, tokens, top_k)) return r;
+    if (zipccl_status r = check_rows(dlogits, tokens, uint64_t(num_experts), dlogits_stride, dtype)) return r;
+    if (!counts != !dloss || (tokens > 0 && !dweights && !dloss)) return ZIPCCL_ERR_INVALID;
+    if (!aligned(dweights, 4) || !aligned(counts, 4) || !aligned(dloss, 4)) return ZIPCCL_ERR_ALIGN;
+    if (tokens == 0) return ZIPCCL_OK;
+    GateArgs a = gate_args(logits, dtype, stride, tokens, num_experts, mask, top_k, status);
+    a.renormalize = renormalize != 0;
+    a.ids = experts;
+    a.id_stride = id_stride;
+    a.wide_ids = id_bytes == 8;
+    a.dweights = dweights;
+    a.totals = counts;
+    a.dloss = dloss;
+    a.dlogits = static_cast<uint8_t*>(dlogits);
+    a.dstride = dlogits_stride;
+    return hip_status(launch_moe_gate_backward(a, static_cast<hipStream_t>(stream)));
+}
+
+uint64_t zipccl_weights4_size(int num_experts, uint64_t outputs, uint64_t row_len)
+{
+    if (num_experts < 1 || num_experts > kMaxExperts || outputs >= kMaxOutputs || row_len > kMaxRowLen4) return 0;
+    return uint64_t(num_experts) * ((outputs + kTile4 - 1) / kTile4) * ((row_len + kSlab4 - 1) / kSlab4) * kTileBytes4;
+}
+
+zipccl_status zipccl_quantize_weights4(const void* w, uint64_t w_stride, int num_experts, uint64_t outputs,
+                                       uint64_t row_len, uint64_t group, void* q, void* scales, int scale_dtype,
+                                       void* stream)
+{
+    if (!is_dtype(scale_dtype) || !is_group(group) || num_experts < 1 || num_experts > kMaxExperts || outputs < 1 ||
+        row_len < 1 || !w || !q || !scales)
+        return ZIPCCL_ERR_INVALID;
+    if (outputs >= kMaxOutputs || row_len > kMaxRowLen4) return ZIPCCL_ERR_SIZE;
+    if (zipccl_status r = check_rows(w, uint64_t(num_experts) * outputs, row_len, w_stride, ZIPCCL_BF16)) return r;
+    if (!aligned(q, 16) || !aligned(scales, value_bytes(scale_dtype))) return ZIPCCL_ERR_ALIGN;
+    Pack4Args a{};
+    a.w = static_cast<const uint16_t*>(w);
+    a.q = static_cast<uint8_t*>(q);
+    a.scales = static_cast<uint8_t*>(scales);
+    a.w_stride = w_stride;
+    a.experts = uint32_t(num_experts);
+    a.outputs = uint32_t(outputs);
+    a.row_len = uint32_t(row_len);
+    a.group = uint32_t(group < kMaxRowLen4 ? group : kMaxRowLen4);   // one group in any case
+    a.fp32 = scale_dtype == ZIPCCL_FP32;
+    return hip_status(launch_quantize_weights4(a, static_cast<hipStream_t>(stream)));
+}
+
+zipccl_status zipccl_experts_product4(const void* x, uint64_t x_stride, uint64_t x_rows, const int32_t* index,
+                                      uint64_t rows, const void* q, const void* scales, int scale_dtype,
+                                      uint64_t group, int num_experts, uint64_t outputs, uint64_t row_len,
+                                      const int32_t* offsets, void* out, uint64_t out_stride, int out_dtype,
+                                      uint32_t* status, void* stream)
+{
+    if (!is_dtype(scale_dtype) || !is_dtype(out_dtype) || !is_group(group) || num_experts < 1 ||
+        num_experts > kMaxExperts || outputs < 1 || row_len < 1 || !q || !scales)
+        return ZIPCCL_ERR_INVALID;
+    if ((!offsets && num_experts != 1) || (!index && rows != x_rows)) return ZIPCCL_ERR_INVALID;
+    if (rows >= kMaxCount || x_rows >= kMaxCount || outputs >= kMaxOutputs || row_len > kMaxRowLen4)
+        return ZIPCCL_ERR_SIZE;
+    if (zipccl_status r = check_rows(x, x_rows, row_len, x_stride, ZIPCCL_BF16)) return r;
+    if (zipccl_status r = check_rows(out, rows, outputs, out_stride, out_dtype)) return r;
+    if (!aligned(q, 16) || !aligned(scales, value_bytes(scale_dtype)) || !aligned(index, 4) || !aligned(offsets, 4) ||
+        (status && !aligned(status, 4)))
+        return ZIPCCL_ERR_ALIGN;
+    if (rows == 0) return ZIPCCL_OK;
+    Product4Args a{};
+    a.x = static_cast<const uint16_t*>(x);
+    a.index = index;
+    a.q = static_cast<const uint8_t*>(q);
+    a.scales = static_cast<const uint8_t*>(scales);
+    a.offsets = offsets;
+    a.out = static_cast<uint8_t*>(out);
+    a.status = status;
+    a.x_stride = x_stride;
+    a.out_stride = out_stride;
+    a.x_rows = uint32_t(x_rows);
+    a.rows = uint32_t(rows);
+    a.experts = uint32_t(num_experts);
+    a.outputs = uint32_t(outputs);
+    a.row_len = uint32_t(row_len);
+    a.slabs = uint32_t((row_len + kSlab4 - 1) / kSlab4);
+    a.group = uint32_t(group < kMaxRowLen4 ? group : kMaxRowLen4);   // one group in any case
+    a.groups = uint32_t((row_len + a.group - 1) / a.group);
+    a.scales_fp32 = scale_dtype == ZIPCCL_FP32;
+    a.fp32 = out_dtype == ZIPCCL_FP32;
+    if (product4_workgroups(a) >= kMaxTiles) return ZIPCCL_ERR_SIZE;
+    return hip_status(launch_experts_product4(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -95,4 +95,80 @@ struct ProductArgs {
 uint64_t product_workgroups(const ProductArgs& a);
 hipError_t launch_experts_product(const ProductArgs& a, hipStream_t s);
 
+// ---- router: choices and weights from logits, balance loss, gradients ----
+constexpr uint32_t kGateBlocks = 256;    // workgroups that leave sums in the workspace
+// per workgroup: sums of probabilities and counts of kMaxExperts experts, and the tokens counted
+constexpr uint64_t kGateWorkspace = uint64_t(kGateBlocks) * (8 * kMaxExperts + 16);
+
+struct GateArgs {
+    const uint8_t* logits;   // tokens x experts
+    const uint8_t* mask;     // tokens, 0: the token takes no part; or null
+    const void* ids;         // choices that are given (balance, gradient): int32 or int64; or null
+    const float* dweights;   // gradient: tokens x top_k, or null
+    const float* dloss;      // gradient: one value, or null
+    const int32_t* totals;   // gradient: counts of the forward pass (experts + 1), or null
+    int32_t* experts;        // choices made: tokens x top_k
+    float* weights;          // tokens x top_k
+    int32_t* counts;         // experts + 1 (the last: tokens counted), or null: no balance outputs
+    float* sums;             // experts
+    float* loss;             // one value
+    uint8_t* dlogits;        // gradient
+    uint8_t* workspace;      // kGateWorkspace bytes, where counts is not null
+    uint32_t* status;        // or null
+    uint64_t stride;         // of logits, values
+    uint64_t dstride;        // of dlogits, values
+    uint64_t id_stride;      // of ids, values
+    uint64_t tokens;
+    uint32_t num_experts;
+    uint32_t top_k;
+    uint32_t renormalize;    // weights sum to 1 over a token's choices; else they are probabilities
+    uint32_t fp32;           // logits and dlogits: 1 fp32, 0 BF16
+    uint32_t wide_ids;       // ids: 1 int64
+    uint32_t blocks;         // workgroups whose sums the workspace holds
+};
+hipError_t launch_moe_gate(const GateArgs& a, hipStream_t s);            // makes choices, or counts those given
+hipError_t launch_moe_gate_backward(const GateArgs& a, hipStream_t s);
+
+// ---- 4-bit weights and their product ----
+constexpr uint32_t kTile4 = 16;          // outputs of a tile of packed weights
+constexpr uint32_t kSlab4 = 128;         // inputs of it
+constexpr uint32_t kTileBytes4 = kTile4 * kSlab4 / 2;
+
+struct Pack4Args {
+    const uint16_t* w;       // BF16, experts * outputs rows
+    uint8_t* q;              // tiles
+    uint8_t* scales;         // experts x groups x outputs
+    uint64_t w_stride;       // values
+    uint32_t experts;
+    uint32_t outputs;
+    uint32_t row_len;
+    uint32_t group;
+    uint32_t fp32;           // scales: 1 fp32, 0 BF16
+};
+hipError_t launch_quantize_weights4(const Pack4Args& a, hipStream_t s);
+
+struct Product4Args {
+    const uint16_t* x;       // BF16 rows
+    const int32_t* index;    // row of x for each row, or null: row s itself
+    const uint8_t* q;        // tiles
+    const uint8_t* scales;   // experts x groups x outputs
+    const int32_t* offsets;  // experts + 1, or null: one expert holds every row
+    uint8_t* out;
+    uint32_t* status;
+    uint64_t x_stride;       // values
+    uint64_t out_stride;     // values
+    uint32_t x_rows;
+    uint32_t rows;
+    uint32_t experts;
+    uint32_t outputs;
+    uint32_t row_len;
+    uint32_t slabs;          // row_len in slabs of kSlab4 values
+    uint32_t groups;         // row_len in groups
+    uint32_t group;          // 32, 64 or a multiple of 128
+    uint32_t scales_fp32;    // scales: 1 fp32, 0 BF16
+    uint32_t fp32;           // out: 1 fp32, 0 BF16
+};
+uint64_t product4_workgroups(const Product4Args& a);
+hipError_t launch_experts_product4(const Product4Args& a, hipStream_t s);
+
 }  // namespace zc

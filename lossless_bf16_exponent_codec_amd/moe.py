@@ -1,6 +1,7 @@
-"""A mixture-of-experts layer's row traffic around the codec, from torch: a router's choices
-sorted by expert, tokens dispatched to their experts' rows and combined back with weights
-(differentiable), and experts' weights in 8 bits.
+"""A mixture-of-experts layer's router and row traffic around the codec, from torch: choices,
+weights and a balance loss from the router's logits, the choices sorted by expert, tokens
+dispatched to their experts' rows and combined back with weights (all differentiable), and
+experts' weights in 8 or 4 bits.
 
 Each step is one call of the same name in `zipccl`; this module adds the buffers and the
 gradients (of first order).  A status word (int32, on the device) given to a step takes the
@@ -17,7 +18,92 @@ from torch.autograd.function import once_differentiable
 
 from . import zipccl as Z
 
-__all__ = ["Routing", "route", "dispatch", "combine", "QuantizedRows", "quantize", "QuantizedExperts"]
+__all__ = ["Gate", "gate", "balance", "Routing", "route", "dispatch", "combine", "QuantizedRows", "quantize",
+           "QuantizedExperts", "pack4", "QuantizedExperts4"]
+
+
+@dataclass
+class Gate:
+    """A router's choices (int32, tokens x top_k, largest logit first, -1: none) and their
+    weights (float32), and, where they were asked for, the balance loss and the counts (int32:
+    choices of each expert, then the number of tokens counted)."""
+    experts: torch.Tensor
+    weights: torch.Tensor
+    loss: torch.Tensor | None = None
+    counts: torch.Tensor | None = None
+
+
+def _balance_buffers(num_experts, device):
+    return (torch.empty(num_experts + 1, dtype=torch.int32, device=device),
+            torch.empty(num_experts, dtype=torch.float32, device=device),
+            torch.empty((), dtype=torch.float32, device=device),
+            torch.empty(Z.MOE_GATE_WORKSPACE_BYTES, dtype=torch.uint8, device=device))
+
+
+def _gate_gradient(logits, experts, mask, renormalize, dweights, counts, dloss, status):
+    if dweights is None and dloss is None:
+        return None
+    dlogits = logits.new_empty(logits.shape)
+    Z.moe_gate_backward(logits, experts, dlogits, None if dweights is None else dweights.contiguous(),
+                        None if dloss is None else counts, dloss, renormalize, mask, status)
+    return dlogits
+
+
+class _Gate(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, top_k, renormalize, mask, with_balance, status):
+        dev = logits.device
+        experts = torch.empty(logits.shape[0], top_k, dtype=torch.int32, device=dev)
+        weights = torch.empty(logits.shape[0], top_k, dtype=torch.float32, device=dev)
+        counts, sums, loss, space = _balance_buffers(logits.shape[1], dev) if with_balance else (None,) * 4
+        Z.moe_gate(logits, experts, weights, renormalize, mask, counts, sums, loss, space, status)
+        ctx.save_for_backward(logits, experts, mask, counts)
+        ctx.renormalize, ctx.status = renormalize, status
+        ctx.set_materialize_grads(False)
+        ctx.mark_non_differentiable(experts, *(() if counts is None else (counts,)))
+        return experts, weights, loss, counts
+
+    @staticmethod
+    @once_differentiable   # the kernels write past autograd: a second derivative is an error
+    def backward(ctx, _, dweights, dloss, __):
+        logits, experts, mask, counts = ctx.saved_tensors
+        return _gate_gradient(logits, experts, mask, ctx.renormalize, dweights, counts, dloss,
+                              ctx.status), None, None, None, None, None
+
+
+class _Balance(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, experts, mask, status):
+        counts, sums, loss, space = _balance_buffers(logits.shape[1], logits.device)
+        Z.moe_balance(logits, experts, counts, sums, loss, space, mask, status)
+        ctx.save_for_backward(logits, experts, mask, counts)
+        ctx.status = status
+        ctx.set_materialize_grads(False)
+        ctx.mark_non_differentiable(counts)
+        return loss, counts
+
+    @staticmethod
+    @once_differentiable   # the kernels write past autograd: a second derivative is an error
+    def backward(ctx, dloss, _):
+        logits, experts, mask, counts = ctx.saved_tensors
+        return _gate_gradient(logits, experts, mask, True, None, counts, dloss, ctx.status), None, None, None
+
+
+def gate(logits: torch.Tensor, top_k: int, renormalize: bool = True, mask=None, balance: bool = False,
+         status=None) -> Gate:
+    """The top_k experts of each token by its logits (tokens x experts, bfloat16 or float32),
+    the lowest number first among equals, and their weights: softmax probabilities, or, with
+    renormalize, those over their sum.  Logits of minus infinity close an expert; mask (bool,
+    one per token) leaves out tokens that are padding.  balance: also the loss that spreads
+    tokens over the experts, experts / (top_k n^2) * sum of counts * probabilities over the n
+    tokens counted.  Differentiable in the logits through weights and loss."""
+    return Gate(*_Gate.apply(logits, top_k, renormalize, mask, balance, status))
+
+
+def balance(logits: torch.Tensor, experts: torch.Tensor, mask=None, status=None):
+    """(loss, counts) as from gate(balance=True), for choices made otherwise (int32 or int64,
+    tokens x top_k, negative ones dropped); the loss is differentiable in the logits."""
+    return _Balance.apply(logits, experts, mask, status)
 
 
 @dataclass
@@ -161,4 +247,62 @@ class QuantizedExperts:
         out = torch.empty(rows.q.shape[0], self.outputs, dtype=dtype, device=rows.q.device)
         Z.experts_product(rows.q, rows.scales, self.q, self.scales, self.inputs, out, offsets=routing.offsets,
                           status=status)
+        return out
+
+
+def pack4(values: torch.Tensor) -> torch.Tensor:
+    """Whole numbers from -8 to 7 (experts x outputs x inputs, any integer type) as 4-bit tiles of
+    16 outputs x 128 inputs: one row of bytes per expert."""
+    E, N, H = values.shape
+    if bool(((values < -8) | (values > 7)).any()):
+        raise ValueError("4-bit values are from -8 to 7")
+    tiles, slabs = -(-N // Z.TILE4_OUTPUTS), -(-H // Z.TILE4_INPUTS)
+    v = torch.zeros(E, tiles * Z.TILE4_OUTPUTS, slabs * Z.TILE4_INPUTS, dtype=torch.uint8, device=values.device)
+    v[:, :N, :H] = (values & 15).to(torch.uint8)
+    v = v.view(E, tiles, 16, slabs, 4, 4, 4, 2)   # ..., output, slab, dword, quarter, byte, half
+    return (v[..., 0] | v[..., 1] << 4).permute(0, 1, 3, 5, 2, 4, 6).reshape(E, -1)
+
+
+class QuantizedExperts4:
+    """Weights of all experts (experts x outputs x inputs, BF16) laid out once in 4 bits with a
+    scale for each output and group of inputs.  Calling it multiplies BF16 rows: each row's
+    token is looked up in x, or, by_expert, x's rows are sorted by expert already."""
+
+    def __init__(self, weights: torch.Tensor, group: int = 128, scale_dtype=torch.bfloat16):
+        self.experts, self.outputs, self.inputs = weights.shape
+        self.group = group
+        if group < 1:
+            raise ValueError("group is 32, 64 or a multiple of 128")
+        self.q = torch.empty(self.experts, Z.weights4_size(1, self.outputs, self.inputs), dtype=torch.uint8,
+                             device=weights.device)
+        self.scales = torch.empty(self.experts, -(-self.inputs // group), self.outputs, dtype=scale_dtype,
+                                  device=weights.device)
+        Z.quantize_weights4(weights, group, self.q, self.scales)
+
+    @classmethod
+    def of(cls, values: torch.Tensor, scales: torch.Tensor, group: int):
+        """From 4-bit values (experts x outputs x inputs, -8 to 7) and scales (experts x outputs x
+        groups, BF16 or FP32) that exist already."""
+        self = cls.__new__(cls)
+        self.experts, self.outputs, self.inputs = values.shape
+        if group < 1 or scales.shape != (self.experts, self.outputs, -(-self.inputs // group)):
+            raise ValueError(f"scales are {tuple(scales.shape)}, values {tuple(values.shape)} in groups of {group}")
+        self.group, self.q, self.scales = group, pack4(values), scales.transpose(1, 2).contiguous()
+        return self
+
+    def __call__(self, x: torch.Tensor, routing: Routing, nrows: int | None = None, by_expert: bool = False,
+                 dtype=torch.bfloat16, status=None) -> torch.Tensor:
+        """nrows: rows of the result (default: the kept choices where splits() has counted them,
+        else all choices; by_expert: x's rows).  Those that no choice has are not set."""
+        if x.shape[1] != self.inputs:
+            raise ValueError(f"rows of {x.shape[1]} values, experts of {self.inputs} inputs")
+        if routing.offsets.numel() != self.experts + 1:
+            raise ValueError(f"{routing.offsets.numel()} offsets, {self.experts} experts")
+        if by_expert:
+            nrows = x.shape[0]
+        elif nrows is None:
+            nrows = routing.rows.numel() if routing.kept is None else routing.kept
+        out = torch.empty(nrows, self.outputs, dtype=dtype, device=x.device)
+        Z.experts_product4(x, self.q, self.scales, self.group, out, rows=None if by_expert else routing.rows,
+                           offsets=routing.offsets, status=status)
         return out

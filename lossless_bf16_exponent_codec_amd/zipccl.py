@@ -20,6 +20,8 @@ STATUS_ESC_OVERFLOW, STATUS_CORRUPT, STATUS_BAD_INDEX, STATUS_WAIT_LIMIT = 1, 2,
 MAX_SEGMENTS, MAX_PEERS = 64, 16
 FORMAT_VERSION, MAGIC = 1, 0x3143435A
 MAX_EXPERTS, MAX_TOP_K, ROW_PAD, MOE_SORT_WORKSPACE_BYTES = 1024, 64, 128, 1 << 20
+MOE_GATE_WORKSPACE_BYTES = 256 * (8 * MAX_EXPERTS + 16)
+TILE4_OUTPUTS, TILE4_INPUTS, TILE4_BYTES = 16, 128, 1024
 BF16, FP32 = 0, 1
 
 
@@ -132,6 +134,20 @@ def _load() -> ctypes.CDLL:
     lib.zipccl_quantize_rows.argtypes = [vp, u64, u64, u64, vp, i32, vp, u64, u64, vp, vp, vp]
     lib.zipccl_experts_product.restype = i32
     lib.zipccl_experts_product.argtypes = [vp, u64, vp, u64, vp, u64, vp, i32, u64, u64, vp, vp, u64, i32, vp, vp]
+    lib.zipccl_moe_gate.restype = i32
+    lib.zipccl_moe_gate.argtypes = [vp, i32, u64, u64, i32, vp, i32, i32, vp, vp, vp, vp, vp, vp, u64, vp, vp]
+    lib.zipccl_moe_balance.restype = i32
+    lib.zipccl_moe_balance.argtypes = [vp, i32, u64, u64, i32, vp, vp, i32, u64, i32, vp, vp, vp, vp, u64, vp, vp]
+    lib.zipccl_moe_gate_backward.restype = i32
+    lib.zipccl_moe_gate_backward.argtypes = [vp, i32, u64, u64, i32, vp, vp, i32, u64, i32, i32, vp, vp, vp, vp, u64,
+                                             vp, vp]
+    lib.zipccl_weights4_size.restype = u64
+    lib.zipccl_weights4_size.argtypes = [i32, u64, u64]
+    lib.zipccl_quantize_weights4.restype = i32
+    lib.zipccl_quantize_weights4.argtypes = [vp, u64, i32, u64, u64, u64, vp, vp, i32, vp]
+    lib.zipccl_experts_product4.restype = i32
+    lib.zipccl_experts_product4.argtypes = [vp, u64, u64, vp, u64, vp, vp, i32, u64, i32, u64, u64, vp, vp, u64, i32,
+                                            vp, vp]
     lib.zipccl_pipeline_scratch_size.restype = u64
     lib.zipccl_pipeline_scratch_size.argtypes = [i32, u64]
     lib.zipccl_pipeline_create.restype = i32
@@ -555,6 +571,8 @@ _VALUES = {torch.bfloat16: BF16, torch.float32: FP32}
 _IDS = {torch.int32: 4, torch.int64: 8}
 _BF16_ONLY = {torch.bfloat16: BF16}
 _INT8 = {torch.int8: 1}
+_INT32 = {torch.int32: 4}
+_BYTES = (torch.bool, torch.uint8)
 
 
 def _matrix(t, what, kinds=_VALUES):
@@ -762,6 +780,144 @@ def experts_product(q, scales, w, w_scales, row_len: int, out, offsets=None, sta
     _enqueue(_lib.zipccl_experts_product, tensors, status, stream,
              (qp, qs, _vector(scales, M, torch.float32, "scales"), M, _vector(w, 0, torch.int8, "w"), ws,
               _vector(w_scales, E * N, torch.float32, "w_scales"), E, N, row_len, starts, op, os_, kind))
+
+
+def _mask(mask, tokens):
+    """Address of one truth value (or byte) per token."""
+    if mask is None:
+        return None
+    if mask.dtype not in _BYTES or not mask.is_contiguous() or mask.shape != (tokens,):
+        raise ValueError(f"mask is a contiguous bool or uint8 tensor of {tokens} values")
+    return mask.data_ptr()
+
+
+def _balance(counts, sums, loss, workspace, num_experts):
+    """Addresses of the balance outputs, and the workspace's with its size."""
+    if not workspace.is_contiguous():
+        raise ValueError("workspace is contiguous")
+    return (_vector(counts, num_experts + 1, torch.int32, "counts"), _vector(sums, num_experts, torch.float32, "sums"),
+            _vector(loss, 1, torch.float32, "loss"), workspace.data_ptr(), workspace.nbytes)
+
+
+def _there(*tensors):
+    return tuple(t for t in tensors if t is not None)
+
+
+def moe_gate(logits, experts, weights, renormalize: bool = True, mask=None, counts=None, sums=None, loss=None,
+             workspace=None, status=None, stream=None):
+    """zipccl_moe_gate.  logits: bfloat16 or float32, tokens x experts.  Writes experts (int32,
+    tokens x top_k) and weights (float32, as many) and, all four given or none, counts (int32,
+    experts + 1), sums (float32, experts) and loss (float32, one value), through workspace
+    (MOE_GATE_WORKSPACE_BYTES device bytes).  mask: bool or uint8, one per token."""
+    zp, T, E, zs, kind = _matrix(logits, "logits")
+    ep, et, K, es, _ = _matrix(experts, "experts", _INT32)
+    if et != T or (es != K and T > 1):
+        raise ValueError(f"experts is a contiguous int32 tensor, tokens x top_k, of {T} tokens")
+    given = _there(counts, sums, loss, workspace)
+    if len(given) not in (0, 4):
+        raise ValueError("counts, sums, loss and workspace are given together")
+    balance = _balance(*given, E) if given else (None, None, None, None, 0)
+    _enqueue(_lib.zipccl_moe_gate, (logits, experts, weights, *given, *_there(mask)), status, stream,
+             (zp, kind, zs, T, E, _mask(mask, T), K, bool(renormalize), ep,
+              _vector(weights, T * K, torch.float32, "weights"), *balance))
+
+
+def moe_balance(logits, experts, counts, sums, loss, workspace, mask=None, status=None, stream=None):
+    """zipccl_moe_balance: counts, sums and loss of given choices (int32 or int64, tokens x
+    top_k, negative: dropped)."""
+    zp, T, E, zs, kind = _matrix(logits, "logits")
+    ep, et, K, es, id_bytes = _matrix(experts, "experts", _IDS)
+    if et != T:
+        _differ(et, T, "the tokens of experts and logits")
+    _enqueue(_lib.zipccl_moe_balance, (logits, experts, counts, sums, loss, workspace, *_there(mask)), status, stream,
+             (zp, kind, zs, T, E, _mask(mask, T), ep, id_bytes, es, K, *_balance(counts, sums, loss, workspace, E)))
+
+
+def moe_gate_backward(logits, experts, dlogits, dweights=None, counts=None, dloss=None, renormalize: bool = True,
+                      mask=None, status=None, stream=None):
+    """zipccl_moe_gate_backward: dlogits (as logits) for dweights (float32, tokens x top_k) and,
+    with the forward call's counts, dloss (float32, one value)."""
+    zp, T, E, zs, kind = _matrix(logits, "logits")
+    dp, dt, de, ds, d_kind = _matrix(dlogits, "dlogits")
+    if (dt, de, d_kind) != (T, E, kind):
+        _differ((dt, de, dlogits.dtype), (T, E, logits.dtype), "dlogits and logits")
+    ep, et, K, es, id_bytes = _matrix(experts, "experts", _IDS)
+    if et != T:
+        _differ(et, T, "the tokens of experts and logits")
+    _enqueue(_lib.zipccl_moe_gate_backward,
+             (logits, experts, dlogits, *_there(dweights, counts, dloss, mask)), status, stream,
+             (zp, kind, zs, T, E, _mask(mask, T), ep, id_bytes, es, K, bool(renormalize),
+              None if dweights is None else _vector(dweights, T * K, torch.float32, "dweights"),
+              None if counts is None else _vector(counts, E + 1, torch.int32, "counts"),
+              None if dloss is None else _vector(dloss, 1, torch.float32, "dloss"), dp, ds))
+
+
+def weights4_size(num_experts: int, outputs: int, row_len: int) -> int:
+    """zipccl_weights4_size."""
+    return _lib.zipccl_weights4_size(num_experts, outputs, row_len)
+
+
+def _scales4(scales, E, G, N):
+    """(address, kind) of experts x groups x outputs scales."""
+    kind = _VALUES.get(scales.dtype)
+    if kind is None or not scales.is_contiguous() or scales.numel() != E * G * N:
+        raise ValueError(f"scales are contiguous, bfloat16 or float32, {E} x {G} x {N}")
+    return scales.data_ptr(), kind
+
+
+def quantize_weights4(w, group: int, q, scales, stream=None):
+    """zipccl_quantize_weights4.  w: bfloat16, experts x outputs x inputs (or outputs x inputs);
+    q: uint8, weights4_size bytes; scales: bfloat16 or float32, experts x groups x outputs."""
+    shape = w.shape
+    if len(shape) not in (2, 3):
+        raise ValueError("w is experts x outputs x inputs")
+    E, N, H = shape if len(shape) == 3 else (1, *shape)
+    if len(shape) == 3 and E > 1 and N > 1 and w.stride(0) != N * w.stride(1):
+        raise ValueError("w's experts follow one another")
+    wp, _, _, ws, _ = _matrix(w[0] if len(shape) == 3 else w, "w", _BF16_ONLY)
+    if len(shape) == 3 and E > 1 and N == 1:
+        ws = w.stride(0)
+    if group < 1:
+        raise ValueError("group is 32, 64 or a multiple of 128")
+    sp, kind = _scales4(scales, E, -(-H // group), N)
+    _enqueue_plain(_lib.zipccl_quantize_weights4, (w, q, scales), stream,
+              (wp, ws, E, N, H, group, _vector(q, weights4_size(E, N, H), torch.uint8, "q"), sp, kind))
+
+
+def _enqueue_plain(call, tensors, stream, args):
+    """_enqueue of a call that has no status word."""
+    device = _one_device(tensors)
+    with torch.cuda.device(device):
+        if stream is None:
+            stream = _raw_stream(device)
+        elif not isinstance(stream, int):
+            other = getattr(stream, "device_index", device)
+            if other != device:
+                _differ(other, device, "the GPUs of the stream and the tensors")
+            stream = stream.cuda_stream
+        _check(call(*args, stream), call.__name__)
+
+
+def experts_product4(x, q, scales, group: int, out, rows=None, offsets=None, status=None, stream=None):
+    """zipccl_experts_product4.  x: bfloat16, tokens x inputs; q and scales (bfloat16 or
+    float32): experts' 4-bit weights as quantize_weights4 writes them; out: rows x outputs,
+    bfloat16 or float32, sorted by expert; rows: int32, the token of each row (None: row s of
+    x); offsets: int32, experts + 1 (None: one expert)."""
+    xp, T, H, xs, _ = _matrix(x, "x", _BF16_ONLY)
+    op, M, N, os_, kind = _matrix(out, "out")
+    if group < 1 or H < 1:
+        raise ValueError("group is 32, 64 or a multiple of 128, rows have a value at least")
+    E = 1 if offsets is None else offsets.numel() - 1
+    sp, s_kind = _scales4(scales, E, -(-H // group), N)
+    size = weights4_size(E, N, H)
+    if q.dtype is not torch.uint8 or not q.is_contiguous() or q.numel() != size:
+        raise ValueError(f"q is a contiguous uint8 tensor of {size} bytes")
+    if rows is None and M != T:
+        _differ(M, T, "the rows of out and x")
+    _enqueue(_lib.zipccl_experts_product4, (x, q, scales, out, *_there(rows, offsets)), status, stream,
+             (xp, xs, T, None if rows is None else _vector(rows, M, torch.int32, "rows"), M, q.data_ptr(), sp, s_kind,
+              group, E, N, H, None if offsets is None else _vector(offsets, E + 1, torch.int32, "offsets"), op, os_,
+              kind))
 
 
 # ------------------------------------------------------------------------------------
