@@ -10,8 +10,6 @@
 // which tiles and waves add them does not show.
 #include <hip/hip_runtime.h>
 
-#include <atomic>
-
 #include "zipccl.h"
 #include "zipccl_moe_internal.h"
 #include "zipccl_row_tiles.h"
@@ -461,25 +459,6 @@ __device__ inline void product_tile(const ProductArgs& a, uint8_t* s_ring, uint3
     for (uint32_t at = wm + lane / kPerRow; at < min(wm + 32 * kM, rows); at += 64 / kPerRow) to.one_nan(a, row0 + at);
 }
 
-// Workgroups go to the 8 XCDs in turn; each XCD takes a run of consecutive tiles, and
-// tiles run over kBand row tiles, then over the outputs, so that those an XCD works on at
-// one time share rows and weights in its L2.
-constexpr uint32_t kXcds = 8, kBand = 4;
-
-__device__ inline uint32_t run_of_xcd(uint32_t id, uint32_t total)
-{
-    const uint32_t per = (total + kXcds - 1) / kXcds;
-    return id / kXcds < per ? min(id % kXcds * per + id / kXcds, total) : total;
-}
-
-__device__ inline void tile_at(uint32_t t, uint32_t down, uint32_t across, uint32_t& row_tile, uint32_t& column)
-{
-    const uint32_t band = t / (kBand * across), in = t % (kBand * across);
-    const uint32_t high = min(kBand, down - band * kBand);
-    row_tile = band * kBand + in % high;
-    column = in / high;
-}
-
 template <uint32_t kM, uint32_t kN, uint32_t kSlots, uint32_t kPerCu>
 __global__ __launch_bounds__(kTileThreads, kPerCu) void product_tile_kernel(const ProductArgs a)
 {
@@ -644,24 +623,6 @@ hipError_t launch_quantize_rows(const QuantArgs& a, hipStream_t s)
 }
 
 namespace {
-
-// Allows a kernel the LDS its launch asks for (past the 64 KB a launch has by default),
-// once per device: the call costs as much as the checks of a launch.
-template <auto kKernel>
-hipError_t allow_lds(uint32_t bytes)
-{
-    static std::atomic<uint64_t> done{0};   // a bit per device
-    if (bytes <= 65536) return hipSuccess;
-    int device = 0;
-    if (hipError_t e = hipGetDevice(&device)) return e;
-    const uint64_t bit = device < 64 ? 1ull << device : 0;
-    if (done.load(std::memory_order_acquire) & bit) return hipSuccess;
-    if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kKernel),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, int(bytes)))
-        return e;
-    done.fetch_or(bit, std::memory_order_release);
-    return hipSuccess;
-}
 
 uint64_t columns(const ProductArgs& a, uint32_t outs) { return (a.outputs + outs - 1) / outs; }
 
