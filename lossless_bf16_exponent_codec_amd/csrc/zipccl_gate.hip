@@ -24,27 +24,16 @@ namespace zc {
 
 namespace {
 
-constexpr uint32_t kNoKey = 0;           // of minus infinity: never chosen
-
-// Unsigned keys in the order of the values: 0 for minus infinity, NaNs above all, both zeros
-// alike.
-__device__ inline uint32_t key_of(float z)
-{
-    const uint32_t b = __float_as_uint(z + 0.0f);
-    if (z != z) return 0xFFFFFFFFu;
-    const uint32_t k = b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u);
-    return k == 0x007FFFFFu ? kNoKey : k;
-}
-
-__device__ inline float value_of(uint32_t key)
-{
-    if (key == kNoKey) return -__builtin_inff();
-    return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);   // the NaN's key gives a NaN
-}
-
 // exp by the hardware's exp2: off by at most about |x| 2^-24 + 2^-23 of it, for x the distance
 // to the row's largest logit.
 __device__ inline float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f); }
+
+// What lanes of this wave wrote to LDS before can be read by its other lanes after.
+__device__ inline void wave_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
 
 template <int kTurn>
 __device__ inline uint32_t turned(uint32_t v)   // from kTurn lanes on, within 16
@@ -52,39 +41,167 @@ __device__ inline uint32_t turned(uint32_t v)   // from kTurn lanes on, within 1
     return uint32_t(__builtin_amdgcn_update_dpp(int(v), int(v), 0x120 + kTurn, 0xF, 0xF, false));
 }
 
+// ---- keys: unsigned 32 bits in the order of the values, NaNs above all, both zeros alike ----
+constexpr uint32_t kClosed = 0x007FFFFFu;    // minus infinity's; 0: a place without a value
+
+__device__ inline uint32_t bits_of(float z)
+{
+    const uint32_t b = __float_as_uint(z + 0.0f);
+    return b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u);
+}
+
+__device__ inline float value_of(uint32_t key)
+{
+    return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);   // a NaN's key gives a NaN
+}
+
+// A key with its expert, so that the largest is the one to choose and no two are equal.
+
+// Of BF16 logits 16 bits are the key's: the expert (from 1023 down) takes the lower ones.
+struct KeyBf16 {
+    uint32_t v;
+    __device__ inline KeyBf16() : v(0) {}
+    __device__ inline KeyBf16(uint32_t key, uint32_t expert) : v((key & 0xFFFF0000u) | (0xFFFFu - expert)) {}
+    __device__ inline uint32_t expert() const { return 0xFFFFu - (v & 0xFFFFu); }
+    __device__ inline uint32_t key() const { return v & 0x80000000u ? v & 0xFFFF0000u : v | 0xFFFFu; }
+    __device__ inline bool open() const { return v > (kClosed | 0xFFFFu); }
+    __device__ inline bool same(KeyBf16 o) const { return v == o.v; }
+    static __device__ inline KeyBf16 larger(KeyBf16 a, KeyBf16 b) { a.v = max(a.v, b.v); return a; }
+    static __device__ inline KeyBf16 smaller(KeyBf16 a, KeyBf16 b) { a.v = min(a.v, b.v); return a; }
+    static __device__ inline KeyBf16 either(bool first, KeyBf16 a, KeyBf16 b) { a.v = first ? a.v : b.v; return a; }
+    template <int kTurn> __device__ inline KeyBf16 turn() const { KeyBf16 k; k.v = turned<kTurn>(v); return k; }
+    __device__ inline KeyBf16 across(int mask) const { KeyBf16 k; k.v = uint32_t(__shfl_xor(int(v), mask)); return k; }
+};
+
+// Of fp32 ones the key and the expert lie in the mantissa of a number from 2 to 4, which the
+// 64-bit maximum and minimum order in one instruction each.
+struct KeyFp32 {
+    double v;
+    __device__ inline KeyFp32() : v(0.0) {}
+    __device__ inline KeyFp32(uint32_t key, uint32_t expert)
+        : v(__hiloint2double(int(0x40000000u | key >> 12), int(key << 20 | (0xFFFFFu - expert)))) {}
+    __device__ inline uint32_t lo() const { return uint32_t(__double2loint(v)); }
+    __device__ inline uint32_t hi() const { return uint32_t(__double2hiint(v)); }
+    __device__ inline uint32_t expert() const { return 0xFFFFFu - (lo() & 0xFFFFFu); }
+    __device__ inline uint32_t key() const { return hi() << 12 | lo() >> 20; }
+    __device__ inline bool open() const { return hi() >= 0x40000000u && key() > kClosed; }
+    __device__ inline bool same(KeyFp32 o) const { return lo() == o.lo(); }     // holds the expert
+    static __device__ inline KeyFp32 larger(KeyFp32 a, KeyFp32 b)
+    {
+        asm("v_max_f64 %0, %1, %2" : "=v"(a.v) : "v"(a.v), "v"(b.v));
+        return a;
+    }
+    static __device__ inline KeyFp32 smaller(KeyFp32 a, KeyFp32 b)
+    {
+        asm("v_min_f64 %0, %1, %2" : "=v"(a.v) : "v"(a.v), "v"(b.v));
+        return a;
+    }
+    static __device__ inline KeyFp32 either(bool first, KeyFp32 a, KeyFp32 b)
+    {
+        a.v = __hiloint2double(first ? int(a.hi()) : int(b.hi()), first ? int(a.lo()) : int(b.lo()));
+        return a;
+    }
+    template <int kTurn> __device__ inline KeyFp32 turn() const
+    {
+        KeyFp32 k;
+        k.v = __hiloint2double(int(turned<kTurn>(hi())), int(turned<kTurn>(lo())));
+        return k;
+    }
+    __device__ inline KeyFp32 across(int mask) const
+    {
+        KeyFp32 k;
+        k.v = __hiloint2double(__shfl_xor(int(hi()), mask), __shfl_xor(int(lo()), mask));
+        return k;
+    }
+};
+
+// The largest of a group's kLanes lanes, in every one of them.
+template <uint32_t kLanes, class Key>
+__device__ inline Key largest(Key k)
+{
+    k = Key::larger(k, k.template turn<8>());
+    k = Key::larger(k, k.template turn<4>());
+    k = Key::larger(k, k.template turn<2>());
+    k = Key::larger(k, k.template turn<1>());
+    if constexpr (kLanes == 64) {
+        k = Key::larger(k, k.across(16));
+        k = Key::larger(k, k.across(32));
+    }
+    return k;
+}
+
 // op over the kLanes lanes of a group, the same bits in every one of them.
 template <uint32_t kLanes, class Op>
-__device__ inline uint32_t across(uint32_t v, Op op)
+__device__ inline float across(float v, Op op)
 {
-    v = op(v, turned<8>(v));
-    v = op(v, turned<4>(v));
-    v = op(v, turned<2>(v));
-    v = op(v, turned<1>(v));
+    const auto with = [&](uint32_t o) { v = op(v, __uint_as_float(o)); };
+    with(turned<8>(__float_as_uint(v)));
+    with(turned<4>(__float_as_uint(v)));
+    with(turned<2>(__float_as_uint(v)));
+    with(turned<1>(__float_as_uint(v)));
     if constexpr (kLanes == 64) {
-        v = op(v, uint32_t(__shfl_xor(int(v), 16)));
-        v = op(v, uint32_t(__shfl_xor(int(v), 32)));
+        with(uint32_t(__shfl_xor(int(__float_as_uint(v)), 16)));
+        with(uint32_t(__shfl_xor(int(__float_as_uint(v)), 32)));
     }
     return v;
 }
 
 template <uint32_t kLanes>
-__device__ inline uint32_t largest(uint32_t v)
-{
-    return across<kLanes>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
-}
-
-template <uint32_t kLanes>
-__device__ inline uint32_t smallest(uint32_t v)
-{
-    return across<kLanes>(v, [](uint32_t a, uint32_t b) { return min(a, b); });
-}
-
-template <uint32_t kLanes>
 __device__ inline float total(float v)
 {
-    return __uint_as_float(across<kLanes>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
-        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
-    }));
+    return across<kLanes>(v, [](float a, float b) { return a + b; });
+}
+
+__device__ inline float larger(float a, float b)    // the one that is a number, if only one is
+{
+    float m;
+    asm("v_max_f32 %0, %1, %2" : "=v"(m) : "v"(a), "v"(b));
+    return m;
+}
+
+// Keys in descending order, by Batcher's odd-even merge exchange.
+template <uint32_t kN, class Key>
+__device__ inline void sort(Key* k)
+{
+#pragma unroll
+    for (uint32_t p = 1; p < kN; p *= 2)
+#pragma unroll
+        for (uint32_t q = p; q > 0; q /= 2)
+#pragma unroll
+            for (uint32_t j = q % p; j + q < kN; j += 2 * q)
+#pragma unroll
+                for (uint32_t i = 0; i < q; i++)
+                    if (i + j + q < kN && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                        const Key a = k[i + j], b = k[i + j + q];
+                        k[i + j] = Key::larger(a, b);
+                        k[i + j + q] = Key::smaller(a, b);
+                    }
+}
+
+// The first kTop of kN keys in descending order (kTop kN, or 8 of 16).
+template <uint32_t kN, uint32_t kTop, class Key>
+__device__ inline void sort_top(Key* k)
+{
+    if constexpr (kTop == kN) {
+        sort<kN>(k);
+    } else {
+        static_assert(kN == 16 && kTop == 8, "two halves");
+        sort<8>(k);
+        sort<8>(k + 8);
+        // of two descending runs, one turned round, the larger ones are the upper half, and rise
+        // and fall once: three rounds of exchanges sort them
+#pragma unroll
+        for (uint32_t i = 0; i < 8; i++) k[i] = Key::larger(k[i], k[15 - i]);
+#pragma unroll
+        for (uint32_t d = 4; d > 0; d /= 2)
+#pragma unroll
+            for (uint32_t i = 0; i < 8; i++)
+                if ((i & d) == 0) {
+                    const Key a = k[i], b = k[i + d];
+                    k[i] = Key::larger(a, b);
+                    k[i + d] = Key::smaller(a, b);
+                }
+    }
 }
 
 // How a row of up to kLanes * kPer values lies over a group's lanes: chunks of kWide
@@ -161,124 +278,142 @@ __device__ inline const uint8_t* row_of(const uint8_t* base, uint64_t token, uin
     return base + token * stride * (fp32 ? 4 : 2);
 }
 
-// A choice that the caller made; -1 for one that is dropped.
-__device__ inline int32_t given(const GateArgs& a, uint64_t token, uint32_t k)
+// A choice that the caller made; -1 for one that is dropped, bad where it is out of range.
+__device__ inline int32_t given(const GateArgs& a, uint64_t token, uint32_t k, bool& bad)
 {
     const uint64_t at = token * a.id_stride + k;
-    int64_t id = a.wide_ids ? static_cast<const int64_t*>(a.ids)[at] : static_cast<const int32_t*>(a.ids)[at];
-    if (id >= int64_t(a.num_experts)) {
-        set_status(a.status, ZIPCCL_STATUS_BAD_INDEX);
-        id = -1;
-    }
-    return id < 0 ? -1 : int32_t(id);
+    const int64_t id = a.wide_ids ? static_cast<const int64_t*>(a.ids)[at] : static_cast<const int32_t*>(a.ids)[at];
+    bad = id >= int64_t(a.num_experts);
+    return id < 0 || bad ? -1 : int32_t(id);
 }
 
-// What a workgroup leaves in the workspace.
+// What a workgroup leaves in the workspace; behind it the words of the finish.
 __device__ inline float* block_sums(const GateArgs& a) { return reinterpret_cast<float*>(a.workspace); }
 __device__ inline uint32_t* block_counts(const GateArgs& a)
 {
     return reinterpret_cast<uint32_t*>(a.workspace) + uint64_t(a.blocks) * a.num_experts;
 }
 __device__ inline uint32_t* block_tokens(const GateArgs& a) { return block_counts(a) + uint64_t(a.blocks) * a.num_experts; }
+__device__ inline uint32_t* finish_ticket(const GateArgs& a) { return block_tokens(a) + kGateBlocks; }
+__device__ inline double* finish_parts(const GateArgs& a) { return reinterpret_cast<double*>(block_tokens(a) + 2 * kGateBlocks); }
+constexpr uint32_t kFinishColumns = 16;
+static_assert(uint64_t(kGateBlocks) * 8 * kMaxExperts + 8 * kGateBlocks + 8 * (kMaxExperts / kFinishColumns) <= kGateWorkspace,
+              "the workspace holds them");
 
-// Forward.  kMake: the choices are made here; else they are given and counted.
-template <uint32_t kLanes, uint32_t kPer, bool kMake>
+__device__ inline float loss_of(const GateArgs& a, uint32_t tokens, double sum)
+{
+    const double n = double(tokens);
+    return tokens ? float(double(a.num_experts) / (double(a.top_k) * n * n) * sum) : 0.0f;
+}
+
+// exp of z less the row's largest, in place, and their sum: 0 for a row without an open
+// expert; a NaN or an infinity makes it a NaN.
+template <uint32_t kLanes, uint32_t kPer>
+__device__ inline float exps(float (&z)[kPer])
+{
+    float most = z[0];
+#pragma unroll
+    for (uint32_t i = 1; i < kPer; i++) most = larger(most, z[i]);
+    most = across<kLanes>(most, [](float a, float b) { return larger(a, b); });
+    const float base = most == -__builtin_inff() ? 0.0f : most;
+    float sum = 0.0f;
+#pragma unroll
+    for (uint32_t i = 0; i < kPer; i++) {
+        z[i] = exp_of(z[i] - base);
+        sum += z[i];
+    }
+    return total<kLanes>(sum);
+}
+
+// Forward.  Key: the choices are made here, for logits of its type; void: they are given, and
+// counted.  kTop: keys of a lane that can be chosen.
+//
+// A lane sorts its keys, then the lanes' firsts are compared top_k times and the one chosen
+// taken off its lane's list.  Bound by the instructions: 16384 x 256 in fp32, 8 of them, take
+// 4096 waves of about 700.
+template <uint32_t kLanes, uint32_t kPer, uint32_t kTop, class Key>
 __global__ __launch_bounds__(1024) void gate_kernel(const GateArgs a)
 {
     using S = Spread<kLanes, kPer>;
     constexpr uint32_t kGroups = 64 / kLanes;
+    constexpr bool kMake = !std::is_void_v<Key>;
     extern __shared__ uint32_t s_count[];     // [expert], then [wave][expert] sums
     __shared__ uint32_t s_tokens;
     const uint32_t lane = lane_id() % kLanes, E = a.num_experts, K = a.top_k;
     const uint32_t waves = blockDim.x / 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const bool fp32 = kMake ? std::is_same_v<Key, KeyFp32> : bool(a.fp32);
     const bool balance = !kMake || a.counts != nullptr;
     if (balance) {
         for (uint32_t e = threadIdx.x; e < E; e += blockDim.x) s_count[e] = 0;
-        if (threadIdx.x == 0) s_tokens = 0;
+        if (threadIdx.x == 0) {
+            s_tokens = 0;
+            if (blockIdx.x == 0) *finish_ticket(a) = 0;
+        }
         __syncthreads();
     }
     float sums[kPer] = {};
     uint32_t tokens = 0;
     const uint64_t step = uint64_t(gridDim.x) * waves * kGroups;
     for (uint64_t t = uint64_t(blockIdx.x) * waves * kGroups + threadIdx.x / kLanes; t < a.tokens; t += step) {
-        const bool there = !a.mask || a.mask[t] != 0;
         float z[kPer];
-        uint32_t key[kPer];
-        if (there) {
-            S::load(z, row_of(a.logits, t, a.stride, a.fp32), lane, E, a.fp32);
-        } else {
+        S::load(z, row_of(a.logits, t, a.stride, fp32), lane, E, fp32);
+        if (a.mask && a.mask[t] == 0) {
 #pragma unroll
             for (uint32_t i = 0; i < kPer; i++) z[i] = -__builtin_inff();
         }
-#pragma unroll
-        for (uint32_t i = 0; i < kPer; i++) key[i] = key_of(z[i]);
-        uint32_t top;          // key of the row's largest
         int32_t id = -1;       // choice `lane`
-        uint32_t id_key = kNoKey;
+        float at_id = 0.0f, top = 0.0f;     // its logit, and the row's largest
         if constexpr (kMake) {
-            top = kNoKey;
+            Key key[kPer];
+            bool nan = false;
+#pragma unroll
+            for (uint32_t i = 0; i < kPer; i++) nan |= z[i] != z[i];
+            if (__any(nan)) {   // as one NaN, of one sign and payload
+#pragma unroll
+                for (uint32_t i = 0; i < kPer; i++) key[i] = Key(z[i] != z[i] ? 0xFFFFFFFFu : bits_of(z[i]), S::expert(lane, i));
+            } else {
+#pragma unroll
+                for (uint32_t i = 0; i < kPer; i++) key[i] = Key(bits_of(z[i]), S::expert(lane, i));
+            }
+            sort_top<kPer, kTop>(key);
             for (uint32_t k = 0; k < K; k++) {
-                uint32_t best = kNoKey, at = 0;
+                const Key best = largest<kLanes>(key[0]);
+                if (!best.open()) break;
+                const bool mine = key[0].same(best);
 #pragma unroll
-                for (uint32_t i = 0; i < kPer; i++)
-                    if (key[i] > best) {
-                        best = key[i];
-                        at = i;
-                    }
-                const uint32_t most = largest<kLanes>(best);
-                if (most == kNoKey) break;
-                const uint32_t mine = best == most ? S::expert(lane, at) : 0xFFFFFFFFu;
-                const uint32_t winner = smallest<kLanes>(mine);
-#pragma unroll
-                for (uint32_t i = 0; i < kPer; i++)
-                    if (S::expert(lane, i) == winner) key[i] = kNoKey;
-                if (k == 0) top = most;
+                for (uint32_t i = 0; i + 1 < kTop; i++) key[i] = Key::either(mine, key[i + 1], key[i]);
+                key[kTop - 1] = Key::either(mine, Key(), key[kTop - 1]);
+                const float v = value_of(best.key());
+                if (k == 0) top = v;
                 if (lane == k) {
-                    id = int32_t(winner);
-                    id_key = most;
+                    id = int32_t(best.expert());
+                    at_id = v;
                 }
             }
-        } else {
-            uint32_t best = kNoKey;
-#pragma unroll
-            for (uint32_t i = 0; i < kPer; i++) best = max(best, key[i]);
-            top = largest<kLanes>(best);
         }
-        const float z0 = value_of(top);
-        const bool some = top != kNoKey;
-        float over = 1.0f;     // 1 / the sum of exp over the row
+        float sum = 0.0f;
         if (balance || !a.renormalize) {
-            float sum = 0.0f;
-#pragma unroll
-            for (uint32_t i = 0; i < kPer; i++) {
-                z[i] = some ? exp_of(z[i] - z0) : 0.0f;
-                sum += z[i];
-            }
-            sum = total<kLanes>(sum);
-            over = some ? 1.0f / sum : 1.0f;
-            if (balance) {
+            sum = exps<kLanes>(z);
+            if (balance && !(sum == 0.0f)) {
+                const float over = 1.0f / sum;
 #pragma unroll
                 for (uint32_t i = 0; i < kPer; i++) sums[i] += z[i] * over;
-                if (some && lane == 0) tokens++;
+                if (lane == 0) tokens++;
             }
         }
         if constexpr (kMake) {
-            const float e = id >= 0 ? exp_of(value_of(id_key) - z0) : 0.0f;
-            float w;
-            if (a.renormalize) {
-                const float sum = total<kLanes>(e);
-                w = some ? e / sum : 0.0f;
-            } else {
-                w = e * over;
-            }
+            const float e = id >= 0 ? exp_of(at_id - top) : 0.0f;
+            if (a.renormalize) sum = total<kLanes>(e);
             if (lane < K) {
                 a.experts[t * K + lane] = id;
-                a.weights[t * K + lane] = w;
+                a.weights[t * K + lane] = id >= 0 ? e / sum : 0.0f;
             }
             if (balance && id >= 0) atomicAdd(&s_count[id], 1u);
-        } else if (some) {
+        } else if (!(sum == 0.0f)) {
             for (uint32_t k = lane; k < K; k += kLanes) {
-                const int32_t g = given(a, t, k);
+                bool bad;
+                const int32_t g = given(a, t, k, bad);
+                if (bad) set_status(a.status, ZIPCCL_STATUS_BAD_INDEX);
                 if (g >= 0) atomicAdd(&s_count[g], 1u);
             }
         }
@@ -306,60 +441,80 @@ __global__ __launch_bounds__(1024) void gate_kernel(const GateArgs a)
     if (threadIdx.x == 0) block_tokens(a)[blockIdx.x] = s_tokens;
 }
 
-// The workgroups' sums and counts joined, and the loss: one workgroup, `shares` threads per
-// expert.
-__global__ __launch_bounds__(1024) void gate_finish_kernel(const GateArgs a)
+// The workgroups' sums and counts joined, 16 experts by each workgroup; the last one to be done
+// adds up the loss.
+__global__ __launch_bounds__(256) void gate_finish_kernel(const GateArgs a)
 {
-    __shared__ double s_sum[1024];
-    __shared__ uint32_t s_number[1024];
-    __shared__ uint32_t s_tokens;
-    const uint32_t tid = threadIdx.x, E = a.num_experts, shares = 1024 / E;
-    const uint32_t e = tid % E, share = tid / E;
+    constexpr uint32_t kShares = 256 / kFinishColumns, kBatch = 8;
+    __shared__ double s_sum[kShares][kFinishColumns];
+    __shared__ uint32_t s_number[kShares][kFinishColumns], s_tokens;
+    const uint32_t tid = threadIdx.x, E = a.num_experts;
+    const uint32_t column = tid % kFinishColumns, share = tid / kFinishColumns;
+    const uint32_t e = blockIdx.x * kFinishColumns + column, at = min(e, E - 1);
     if (tid == 0) s_tokens = 0;
     double sum = 0.0;
     uint32_t number = 0;
-    if (share < shares) {
-#pragma unroll 8
-        for (uint32_t b = share; b < a.blocks; b += shares) {
-            sum += double(block_sums(a)[uint64_t(b) * E + e]);
-            number += block_counts(a)[uint64_t(b) * E + e];
+    for (uint32_t b0 = 0; b0 < a.blocks; b0 += kBatch * kShares) {
+        float f[kBatch];
+        uint32_t n[kBatch];
+#pragma unroll
+        for (uint32_t j = 0; j < kBatch; j++) {
+            const uint64_t from = uint64_t(min(b0 + j * kShares + share, a.blocks - 1)) * E + at;
+            f[j] = block_sums(a)[from];
+            n[j] = block_counts(a)[from];
         }
+#pragma unroll
+        for (uint32_t j = 0; j < kBatch; j++)
+            if (b0 + j * kShares + share < a.blocks) {
+                sum += double(f[j]);
+                number += n[j];
+            }
     }
-    s_sum[tid] = sum;
-    s_number[tid] = number;
+    s_sum[share][column] = sum;
+    s_number[share][column] = number;
+    const uint32_t tokens = tid < a.blocks ? block_tokens(a)[tid] : 0;
+    static_assert(kGateBlocks <= 256, "a thread for each workgroup");
     __syncthreads();
-    uint32_t tokens = 0;
-    for (uint32_t b = tid; b < a.blocks; b += 1024) tokens += block_tokens(a)[b];
     if (tokens) atomicAdd(&s_tokens, tokens);
-    double part = 0.0;
-    if (tid < E) {
-        for (uint32_t s = 1; s < shares; s++) {
-            sum += s_sum[s * E + tid];
-            number += s_number[s * E + tid];
+    if (tid < kFinishColumns) {
+        for (uint32_t s = 1; s < kShares; s++) {
+            sum += s_sum[s][tid];
+            number += s_number[s][tid];
         }
-        a.sums[tid] = float(sum);
-        a.counts[tid] = int32_t(number);
-        part = double(number) * sum;
+        double part = 0.0;
+        if (e < E) {
+            a.sums[e] = float(sum);
+            a.counts[e] = int32_t(number);
+            part = double(number) * sum;
+        }
+        s_sum[0][tid] = part;
     }
     __syncthreads();
-    s_sum[tid] = part;
-    for (uint32_t d = 512; d > 0; d >>= 1) {
-        __syncthreads();
-        if (tid < d) s_sum[tid] += s_sum[tid + d];
+    if (tid != 0) return;
+    double all = 0.0;
+    for (uint32_t c = 0; c < kFinishColumns; c++) all += s_sum[0][c];
+    if (blockIdx.x == 0) a.counts[E] = int32_t(s_tokens);
+    if (gridDim.x > 1) {
+        __hip_atomic_store(finish_parts(a) + blockIdx.x, all, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const uint32_t before = __hip_atomic_fetch_add(finish_ticket(a), 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+        if (before + 1 != gridDim.x) return;
+        all = 0.0;
+        for (uint32_t b = 0; b < gridDim.x; b++)
+            all += __hip_atomic_load(finish_parts(a) + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    if (tid == 0) {
-        const double n = double(s_tokens);
-        a.counts[E] = int32_t(s_tokens);
-        a.loss[0] = s_tokens ? float(double(E) / (double(a.top_k) * n * n) * s_sum[0]) : 0.0f;
-    }
+    a.loss[0] = loss_of(a, s_tokens, all);
 }
 
-template <uint32_t kLanes, uint32_t kPer>
+// The choices' gradients come to the lanes that hold their columns through a row of LDS for
+// each token at hand, all zeros but for them.
+template <uint32_t kLanes, uint32_t kPer, bool kFp32>
 __global__ __launch_bounds__(256) void gate_backward_kernel(const GateArgs a)
 {
     using S = Spread<kLanes, kPer>;
     constexpr uint32_t kGroups = 64 / kLanes;
+    __shared__ __attribute__((aligned(16))) float s_rows[256 * kPer];
     const uint32_t lane = lane_id() % kLanes, E = a.num_experts, K = a.top_k;
+    float* s_row = s_rows + threadIdx.x / kLanes * (kLanes * kPer);
     float f[kPer] = {};        // gradient of the loss by the probabilities
     if (a.totals) {
         const float n = float(a.totals[E]);
@@ -370,75 +525,92 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(const GateArgs a)
             if (e < E) f[i] = per * float(a.totals[e]);
         }
     }
+    if (a.dweights)
+        for (uint32_t i = 0; i < kPer; i++) s_row[lane + i * kLanes] = 0.0f;
     const uint64_t step = uint64_t(gridDim.x) * 4 * kGroups;
     for (uint64_t t = uint64_t(blockIdx.x) * 4 * kGroups + threadIdx.x / kLanes; t < a.tokens; t += step) {
-        uint8_t* out = const_cast<uint8_t*>(row_of(a.dlogits, t, a.dstride, a.fp32));
-        const uint8_t* row = row_of(a.logits, t, a.stride, a.fp32);
+        uint8_t* out = const_cast<uint8_t*>(row_of(a.dlogits, t, a.dstride, kFp32));
+        const uint8_t* row = row_of(a.logits, t, a.stride, kFp32);
         float z[kPer], add[kPer] = {};
-        uint32_t top = kNoKey;
-        if (!a.mask || a.mask[t] != 0) {
-            S::load(z, row, lane, E, a.fp32);
-#pragma unroll
-            for (uint32_t i = 0; i < kPer; i++) top = max(top, key_of(z[i]));
-            top = largest<kLanes>(top);
+        S::load(z, row, lane, E, kFp32);
+        const bool there = !a.mask || a.mask[t] != 0;
+        int32_t id = -1;       // choice `lane`, its gradient and its logit
+        float d = 0.0f, c = -__builtin_inff();
+        bool bad = false;
+        if (a.dweights && lane < K && there) {
+            id = given(a, t, lane, bad);
+            if (id >= 0) {
+                d = a.dweights[t * K + lane];
+                if (a.renormalize) c = kFp32 ? reinterpret_cast<const float*>(row)[id]
+                                             : __uint_as_float(uint32_t(reinterpret_cast<const uint16_t*>(row)[id]) << 16);
+            }
         }
-        if (top == kNoKey) {
-            S::store(add, out, lane, E, a.fp32);
+        if (!there) {
+#pragma unroll
+            for (uint32_t i = 0; i < kPer; i++) z[i] = -__builtin_inff();
+        }
+        const float sum = exps<kLanes>(z);
+        if (sum == 0.0f) {     // nothing open
+            S::store(add, out, lane, E, kFp32);
             continue;
         }
-        const float z0 = value_of(top);
-        float sum = 0.0f;
-#pragma unroll
-        for (uint32_t i = 0; i < kPer; i++) {
-            z[i] = exp_of(z[i] - z0);
-            sum += z[i];
-        }
-        const float over = 1.0f / total<kLanes>(sum);
-        float g[kPer];
-#pragma unroll
-        for (uint32_t i = 0; i < kPer; i++) {
-            z[i] *= over;
-            g[i] = f[i];
-        }
+        const float over = 1.0f / sum;
+        if (bad) set_status(a.status, ZIPCCL_STATUS_BAD_INDEX);
         if (a.dweights) {
-            int32_t id = lane < K ? given(a, t, lane) : -1;
-            float d = id >= 0 ? a.dweights[t * K + lane] : 0.0f;
             if (a.renormalize) {
-                float c = -__builtin_inff();
-                if (id >= 0) c = a.fp32 ? reinterpret_cast<const float*>(row)[id]
-                                        : __uint_as_float(uint32_t(reinterpret_cast<const uint16_t*>(row)[id]) << 16);
-                const uint32_t most = largest<kLanes>(key_of(c));
-                const float e = id >= 0 && most != kNoKey ? exp_of(c - value_of(most)) : 0.0f;
+                const float most = across<kLanes>(c, [](float x, float y) { return larger(x, y); });
+                const float e = exp_of(c - (most == -__builtin_inff() ? 0.0f : most));
                 const float all = total<kLanes>(e);
-                const float w = most != kNoKey ? e / all : 0.0f;
-                const float dot = total<kLanes>(w * d);
-                d = w * (d - dot);
+                const float w = all == 0.0f ? 0.0f : e / all;
+                d = w * (d - total<kLanes>(w * d));
             }
-            for (uint32_t k = 0; k < K; k++) {
-                const int32_t at = __shfl(id, int(k), int(kLanes));
-                const float v = __shfl(d, int(k), int(kLanes));
-                if (at < 0) continue;
+            // a lane whose number another one has overwritten shares its expert: then one after the
+            // other adds
+            const bool chosen = id >= 0;
+            if (chosen) s_row[id] = __uint_as_float(lane + 1);
+            wave_order();
+            const bool shared = chosen && __float_as_uint(s_row[id]) != lane + 1;
+            wave_order();
+            if (__any(shared)) {
+                if (chosen) s_row[id] = 0.0f;
+                for (uint32_t k = 0; k < K; k++) {
+                    wave_order();
+                    if (chosen && lane == k) s_row[id] += d;
+                }
+            } else if (chosen) {
+                s_row[id] = d;
+            }
+            wave_order();
 #pragma unroll
-                for (uint32_t i = 0; i < kPer; i++)
-                    if (S::expert(lane, i) == uint32_t(at)) add[i] += v;
-            }
-            if (!a.renormalize) {
+            for (uint32_t i = 0; i < kPer; i += S::kWide) __builtin_memcpy(&add[i], s_row + S::first(lane, i), 4 * S::kWide);
+            wave_order();
+            if (chosen) s_row[id] = 0.0f;
+        }
+        if (a.renormalize) {
+            if (a.totals) {
+                float dot = 0.0f;
 #pragma unroll
                 for (uint32_t i = 0; i < kPer; i++) {
-                    g[i] += add[i];
-                    add[i] = 0.0f;
+                    z[i] *= over;
+                    dot += z[i] * f[i];
                 }
+                dot = total<kLanes>(dot);
+#pragma unroll
+                for (uint32_t i = 0; i < kPer; i++) add[i] += z[i] * (f[i] - dot);
             }
-        }
-        if (a.totals || !a.renormalize) {
+        } else {
             float dot = 0.0f;
 #pragma unroll
-            for (uint32_t i = 0; i < kPer; i++) dot += z[i] * g[i];
+            for (uint32_t i = 0; i < kPer; i++) {
+                z[i] *= over;
+                add[i] += f[i];
+                dot += z[i] * add[i];
+            }
             dot = total<kLanes>(dot);
 #pragma unroll
-            for (uint32_t i = 0; i < kPer; i++) add[i] += z[i] * (g[i] - dot);
+            for (uint32_t i = 0; i < kPer; i++) add[i] = z[i] * (add[i] - dot);
         }
-        S::store(add, out, lane, E, a.fp32);
+        S::store(add, out, lane, E, kFp32);
     }
 }
 
@@ -469,21 +641,24 @@ hipError_t launch_moe_gate(const GateArgs& args, hipStream_t s)
 {
     GateArgs a = args;
     const bool balance = a.counts != nullptr;
-    a.blocks = 0;
-    hipError_t e = by_shape(a, [&](auto lanes, auto per) {
+    const hipError_t e = by_shape(a, [&](auto lanes, auto per) {
         constexpr uint32_t kLanes = decltype(lanes)::value, kPer = decltype(per)::value;
-        if (a.tokens == 0) return hipSuccess;
-        const uint32_t threads = 256, tokens = threads / kLanes;
-        const uint64_t groups = (a.tokens + tokens - 1) / tokens, most = balance ? kGateBlocks : 1u << 20;
-        const uint32_t blocks = uint32_t(groups < most ? groups : most);
+        constexpr uint32_t kTop = kPer < 8 ? kPer : 8;
+        // as many workgroups as the workspace has room for, of as many waves as that leaves
+        uint32_t threads = 256;
+        while (balance && threads < 1024 && a.tokens * kLanes > uint64_t(kGateBlocks) * threads) threads *= 2;
+        if (kLanes == 64) threads = 256;      // their sums in LDS are long
+        const uint64_t tokens = threads / kLanes, groups = (a.tokens + tokens - 1) / tokens, most = balance ? kGateBlocks : 1u << 20;
+        a.blocks = groups == 0 ? 1 : uint32_t(groups < most ? groups : most);
         const uint32_t lds = balance ? 4 * a.num_experts * (1 + threads / 64) : 0;
-        a.blocks = blocks;
-        if (a.ids) hipLaunchKernelGGL((gate_kernel<kLanes, kPer, false>), dim3(blocks), dim3(threads), lds, s, a);
-        else hipLaunchKernelGGL((gate_kernel<kLanes, kPer, true>), dim3(blocks), dim3(threads), lds, s, a);
+        const auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(a.blocks), dim3(threads), lds, s, a); };
+        if (a.ids) run(gate_kernel<kLanes, kPer, 1, void>);
+        else if (kTop < kPer && a.top_k > kTop) a.fp32 ? run(gate_kernel<kLanes, kPer, kPer, KeyFp32>) : run(gate_kernel<kLanes, kPer, kPer, KeyBf16>);
+        else a.fp32 ? run(gate_kernel<kLanes, kPer, kTop, KeyFp32>) : run(gate_kernel<kLanes, kPer, kTop, KeyBf16>);
         return hipGetLastError();
     });
     if (e != hipSuccess || !balance) return e;
-    hipLaunchKernelGGL(gate_finish_kernel, dim3(1), dim3(1024), 0, s, a);
+    hipLaunchKernelGGL(gate_finish_kernel, dim3((a.num_experts + kFinishColumns - 1) / kFinishColumns), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -493,8 +668,9 @@ hipError_t launch_moe_gate_backward(const GateArgs& a, hipStream_t s)
         constexpr uint32_t kLanes = decltype(lanes)::value, kPer = decltype(per)::value;
         constexpr uint32_t kTokens = 256 / kLanes;
         const uint64_t groups = (a.tokens + kTokens - 1) / kTokens;
-        hipLaunchKernelGGL((gate_backward_kernel<kLanes, kPer>), dim3(uint32_t(groups < (1u << 20) ? groups : 1u << 20)),
-                           dim3(256), 0, s, a);
+        const dim3 grid(uint32_t(groups < (1u << 20) ? groups : 1u << 20));
+        if (a.fp32) hipLaunchKernelGGL((gate_backward_kernel<kLanes, kPer, true>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((gate_backward_kernel<kLanes, kPer, false>), grid, dim3(256), 0, s, a);
         return hipGetLastError();
     });
 }
