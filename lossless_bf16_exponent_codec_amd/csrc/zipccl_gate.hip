@@ -212,32 +212,47 @@ struct Spread {
     static __device__ inline uint32_t first(uint32_t lane, uint32_t i) { return (i / kWide * kLanes + lane) * kWide; }
     static __device__ inline uint32_t expert(uint32_t lane, uint32_t i) { return first(lane, i) + i % kWide; }
 
-    // z of a row: minus infinity past its end.
+    // z of a row: minus infinity past its end, which no load passes.  No lane branches: loads under
+    // different lanes' branches wait for one another.
     static __device__ inline void load(float (&z)[kPer], const uint8_t* row, uint32_t lane, uint32_t n, bool fp32)
     {
+        if (fp32) load_as<float>(z, reinterpret_cast<const float*>(row), lane, n);
+        else load_as<uint16_t>(z, reinterpret_cast<const uint16_t*>(row), lane, n);
+    }
+
+    static __device__ inline float as_float(float v) { return v; }
+    static __device__ inline float as_float(uint16_t v) { return __uint_as_float(uint32_t(v) << 16); }
+
+    template <class T>
+    static __device__ inline void load_as(float (&z)[kPer], const T* row, uint32_t lane, uint32_t n)
+    {
+        T v[kPer];
+        if (n == kLanes * kPer) {
 #pragma unroll
-        for (uint32_t i = 0; i < kPer; i += kWide) {
-            const uint32_t e = first(lane, i);
-            if (fp32) {
-                const float* at = reinterpret_cast<const float*>(row) + e;
-                if (e + kWide <= n) {
-                    __builtin_memcpy(&z[i], at, 4 * kWide);
-                } else {
+            for (uint32_t i = 0; i < kPer; i += kWide) __builtin_memcpy(&v[i], row + first(lane, i), sizeof(T) * kWide);
 #pragma unroll
-                    for (uint32_t j = 0; j < kWide; j++) z[i + j] = e + j < n ? at[j] : -__builtin_inff();
+            for (uint32_t i = 0; i < kPer; i++) z[i] = as_float(v[i]);
+        } else if (n >= kWide) {
+            // a chunk that the row ends in is the row's last kWide values, moved down
+#pragma unroll
+            for (uint32_t i = 0; i < kPer; i += kWide) __builtin_memcpy(&v[i], row + min(first(lane, i), n - kWide), sizeof(T) * kWide);
+#pragma unroll
+            for (uint32_t i = 0; i < kPer; i += kWide) {
+                const uint32_t e = first(lane, i), moved = e - min(e, n - kWide);
+#pragma unroll
+                for (uint32_t j = 0; j < kWide; j++) {
+                    float x = as_float(v[i + j]);
+#pragma unroll
+                    for (uint32_t d = 1; d < kWide; d++)
+                        if (j + d < kWide) x = moved == d ? as_float(v[i + j + d]) : x;
+                    z[i + j] = e + j < n ? x : -__builtin_inff();
                 }
-            } else {
-                const uint16_t* at = reinterpret_cast<const uint16_t*>(row) + e;
-                uint16_t b[kWide];
-                if (e + kWide <= n) {
-                    __builtin_memcpy(b, at, 2 * kWide);
-                } else {
-#pragma unroll
-                    for (uint32_t j = 0; j < kWide; j++) b[j] = e + j < n ? at[j] : 0xFF80u;
-                }
-#pragma unroll
-                for (uint32_t j = 0; j < kWide; j++) z[i + j] = __uint_as_float(uint32_t(b[j]) << 16);
             }
+        } else {
+#pragma unroll
+            for (uint32_t i = 0; i < kPer; i++) v[i] = row[min(expert(lane, i), n - 1)];
+#pragma unroll
+            for (uint32_t i = 0; i < kPer; i++) z[i] = expert(lane, i) < n ? as_float(v[i]) : -__builtin_inff();
         }
     }
 
@@ -354,10 +369,24 @@ __global__ __launch_bounds__(1024) void gate_kernel(const GateArgs a)
     float sums[kPer] = {};
     uint32_t tokens = 0;
     const uint64_t step = uint64_t(gridDim.x) * waves * kGroups;
-    for (uint64_t t = uint64_t(blockIdx.x) * waves * kGroups + threadIdx.x / kLanes; t < a.tokens; t += step) {
+    uint64_t t = uint64_t(blockIdx.x) * waves * kGroups + threadIdx.x / kLanes;
+    // Short rows are requested one ahead (65536 x 64, given choices: 8.6 us, ).
+    constexpr bool kAhead = kPer <= 4;
+    float ahead[kPer];
+    bool there_ahead = false;
+    const auto load = [&](uint64_t at) {
+        S::load(ahead, row_of(a.logits, at, a.stride, fp32), lane, E, fp32);
+        there_ahead = !a.mask || a.mask[at] != 0;
+    };
+    if (kAhead && t < a.tokens) load(t);
+    for (; t < a.tokens; t += step) {
         float z[kPer];
-        S::load(z, row_of(a.logits, t, a.stride, fp32), lane, E, fp32);
-        if (a.mask && a.mask[t] == 0) {
+        if (!kAhead) load(t);
+#pragma unroll
+        for (uint32_t i = 0; i < kPer; i++) z[i] = ahead[i];
+        const bool there = there_ahead;
+        if (kAhead && t + step < a.tokens) load(t + step);
+        if (!there) {
 #pragma unroll
             for (uint32_t i = 0; i < kPer; i++) z[i] = -__builtin_inff();
         }
@@ -442,71 +471,95 @@ __global__ __launch_bounds__(1024) void gate_kernel(const GateArgs a)
 }
 
 // The workgroups' sums and counts joined, 16 experts by each workgroup; the last one to be done
-// adds up the loss.
-__global__ __launch_bounds__(256) void gate_finish_kernel(const GateArgs a)
+// adds up the loss.  What counts is the chain of steps: one batch of loads for each thread.
+constexpr uint32_t kFinishThreads = 1024;
+
+__global__ __launch_bounds__(kFinishThreads) void gate_finish_kernel(const GateArgs a)
 {
-    constexpr uint32_t kShares = 256 / kFinishColumns, kBatch = 8;
+    constexpr uint32_t kShares = kFinishThreads / kFinishColumns, kBatch = kGateBlocks / kShares;
     __shared__ double s_sum[kShares][kFinishColumns];
     __shared__ uint32_t s_number[kShares][kFinishColumns], s_tokens;
     const uint32_t tid = threadIdx.x, E = a.num_experts;
     const uint32_t column = tid % kFinishColumns, share = tid / kFinishColumns;
     const uint32_t e = blockIdx.x * kFinishColumns + column, at = min(e, E - 1);
     if (tid == 0) s_tokens = 0;
+    float f[kBatch];
+    uint32_t n[kBatch];
+#pragma unroll
+    for (uint32_t j = 0; j < kBatch; j++) {
+        const uint64_t from = uint64_t(min(j * kShares + share, a.blocks - 1)) * E + at;
+        f[j] = block_sums(a)[from];
+        n[j] = block_counts(a)[from];
+    }
+    const uint32_t tokens = tid < a.blocks ? block_tokens(a)[tid] : 0;
+    static_assert(kGateBlocks <= kFinishThreads && kGateBlocks % kShares == 0, "a thread for each workgroup");
     double sum = 0.0;
     uint32_t number = 0;
-    for (uint32_t b0 = 0; b0 < a.blocks; b0 += kBatch * kShares) {
-        float f[kBatch];
-        uint32_t n[kBatch];
 #pragma unroll
-        for (uint32_t j = 0; j < kBatch; j++) {
-            const uint64_t from = uint64_t(min(b0 + j * kShares + share, a.blocks - 1)) * E + at;
-            f[j] = block_sums(a)[from];
-            n[j] = block_counts(a)[from];
+    for (uint32_t j = 0; j < kBatch; j++)
+        if (j * kShares + share < a.blocks) {
+            sum += double(f[j]);
+            number += n[j];
         }
-#pragma unroll
-        for (uint32_t j = 0; j < kBatch; j++)
-            if (b0 + j * kShares + share < a.blocks) {
-                sum += double(f[j]);
-                number += n[j];
-            }
-    }
     s_sum[share][column] = sum;
     s_number[share][column] = number;
-    const uint32_t tokens = tid < a.blocks ? block_tokens(a)[tid] : 0;
-    static_assert(kGateBlocks <= 256, "a thread for each workgroup");
     __syncthreads();
     if (tokens) atomicAdd(&s_tokens, tokens);
+#pragma unroll
+    for (uint32_t d = kShares / 2; d >= 4; d /= 4) {    // four to one
+        if (share < d / 2) {
+            for (uint32_t s = share + d / 2; s < 2 * d; s += d / 2) {
+                sum += s_sum[s][column];
+                number += s_number[s][column];
+            }
+            s_sum[share][column] = sum;
+            s_number[share][column] = number;
+        }
+        __syncthreads();
+    }
+    if (tid >= 64) return;
+    double all = 0.0;
     if (tid < kFinishColumns) {
-        for (uint32_t s = 1; s < kShares; s++) {
+        for (uint32_t s = 1; s < 4; s++) {
             sum += s_sum[s][tid];
             number += s_number[s][tid];
         }
-        double part = 0.0;
         if (e < E) {
             a.sums[e] = float(sum);
             a.counts[e] = int32_t(number);
-            part = double(number) * sum;
+            all = double(number) * sum;
         }
-        s_sum[0][tid] = part;
     }
-    __syncthreads();
-    if (tid != 0) return;
-    double all = 0.0;
-    for (uint32_t c = 0; c < kFinishColumns; c++) all += s_sum[0][c];
-    if (blockIdx.x == 0) a.counts[E] = int32_t(s_tokens);
+    // lanes, then workgroups, in a fixed tree
+    const auto join = [](double v) {
+#pragma unroll
+        for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d);
+        return v;
+    };
+    all = join(all);
+    if (blockIdx.x == 0 && tid == 0) a.counts[E] = int32_t(s_tokens);
     if (gridDim.x > 1) {
-        __hip_atomic_store(finish_parts(a) + blockIdx.x, all, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        const uint32_t before = __hip_atomic_fetch_add(finish_ticket(a), 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-        if (before + 1 != gridDim.x) return;
-        all = 0.0;
-        for (uint32_t b = 0; b < gridDim.x; b++)
-            all += __hip_atomic_load(finish_parts(a) + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        uint32_t before = 0;
+        if (tid == 0) {
+            // both are done where all XCDs see them, the second once the first is; ordering by release
+            // and acquire would write back and drop the L2, 2 us
+            __hip_atomic_store(finish_parts(a) + blockIdx.x, all, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            before = __hip_atomic_fetch_add(finish_ticket(a), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        if (__builtin_amdgcn_readfirstlane(before) + 1 != gridDim.x) return;
+        static_assert(kMaxExperts / kFinishColumns <= 64, "a lane for each workgroup");
+        all = tid < gridDim.x ? __hip_atomic_load(finish_parts(a) + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
+        all = join(all);
     }
-    a.loss[0] = loss_of(a, s_tokens, all);
+    if (tid == 0) a.loss[0] = loss_of(a, s_tokens, all);
 }
 
-// The choices' gradients come to the lanes that hold their columns through a row of LDS for
-// each token at hand, all zeros but for them.
+// What lane and choice agree on is passed through a row of LDS for each token at hand: the
+// probabilities to the choices (their weights), then the choices' gradients to their columns.
+// The first row and choices are requested before the counts, which every row needs.
+//
+// Bound by memory and the chain of its latencies.
 template <uint32_t kLanes, uint32_t kPer, bool kFp32>
 __global__ __launch_bounds__(256) void gate_backward_kernel(const GateArgs a)
 {
@@ -515,58 +568,78 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(const GateArgs a)
     __shared__ __attribute__((aligned(16))) float s_rows[256 * kPer];
     const uint32_t lane = lane_id() % kLanes, E = a.num_experts, K = a.top_k;
     float* s_row = s_rows + threadIdx.x / kLanes * (kLanes * kPer);
+    const auto put = [&](const float (&v)[kPer]) {
+#pragma unroll
+        for (uint32_t i = 0; i < kPer; i += S::kWide) __builtin_memcpy(s_row + S::first(lane, i), &v[i], 4 * S::kWide);
+    };
+    const uint64_t step = uint64_t(gridDim.x) * 4 * kGroups;
+    uint64_t t = uint64_t(blockIdx.x) * 4 * kGroups + threadIdx.x / kLanes;
+    float z[kPer];
+    int32_t id = -1;       // choice `lane`
+    float d = 0.0f;        // and its gradient
+    bool bad = false, there = false;
+    const auto load = [&]() {
+        S::load(z, row_of(a.logits, t, a.stride, kFp32), lane, E, kFp32);
+        there = !a.mask || a.mask[t] != 0;
+        id = -1;
+        d = 0.0f;
+        bad = false;
+        if (a.dweights && lane < K) {
+            id = given(a, t, lane, bad);
+            d = a.dweights[t * K + lane];
+            if (id < 0) d = 0.0f;
+        }
+    };
+    if (t < a.tokens) load();
     float f[kPer] = {};        // gradient of the loss by the probabilities
     if (a.totals) {
+        int32_t count[kPer];
+#pragma unroll
+        for (uint32_t i = 0; i < kPer; i++) count[i] = a.totals[min(S::expert(lane, i), E - 1)];
         const float n = float(a.totals[E]);
         const float per = n > 0.0f ? a.dloss[0] * (float(E) / float(K)) / (n * n) : 0.0f;
 #pragma unroll
-        for (uint32_t i = 0; i < kPer; i++) {
-            const uint32_t e = S::expert(lane, i);
-            if (e < E) f[i] = per * float(a.totals[e]);
-        }
+        for (uint32_t i = 0; i < kPer; i++) f[i] = S::expert(lane, i) < E ? per * float(count[i]) : 0.0f;
     }
-    if (a.dweights)
-        for (uint32_t i = 0; i < kPer; i++) s_row[lane + i * kLanes] = 0.0f;
-    const uint64_t step = uint64_t(gridDim.x) * 4 * kGroups;
-    for (uint64_t t = uint64_t(blockIdx.x) * 4 * kGroups + threadIdx.x / kLanes; t < a.tokens; t += step) {
+    const float none[kPer] = {};
+    if (a.dweights) put(none);
+    for (; t < a.tokens; t += step, t < a.tokens ? load() : void()) {
         uint8_t* out = const_cast<uint8_t*>(row_of(a.dlogits, t, a.dstride, kFp32));
-        const uint8_t* row = row_of(a.logits, t, a.stride, kFp32);
-        float z[kPer], add[kPer] = {};
-        S::load(z, row, lane, E, kFp32);
-        const bool there = !a.mask || a.mask[t] != 0;
-        int32_t id = -1;       // choice `lane`, its gradient and its logit
-        float d = 0.0f, c = -__builtin_inff();
-        bool bad = false;
-        if (a.dweights && lane < K && there) {
-            id = given(a, t, lane, bad);
-            if (id >= 0) {
-                d = a.dweights[t * K + lane];
-                if (a.renormalize) c = kFp32 ? reinterpret_cast<const float*>(row)[id]
-                                             : __uint_as_float(uint32_t(reinterpret_cast<const uint16_t*>(row)[id]) << 16);
-            }
-        }
         if (!there) {
 #pragma unroll
             for (uint32_t i = 0; i < kPer; i++) z[i] = -__builtin_inff();
         }
         const float sum = exps<kLanes>(z);
         if (sum == 0.0f) {     // nothing open
-            S::store(add, out, lane, E, kFp32);
+            S::store(none, out, lane, E, kFp32);
             continue;
         }
-        const float over = 1.0f / sum;
         if (bad) set_status(a.status, ZIPCCL_STATUS_BAD_INDEX);
+        float add[kPer] = {};
         if (a.dweights) {
+            const bool chosen = id >= 0;
             if (a.renormalize) {
-                const float most = across<kLanes>(c, [](float x, float y) { return larger(x, y); });
-                const float e = exp_of(c - (most == -__builtin_inff() ? 0.0f : most));
-                const float all = total<kLanes>(e);
+                wave_order();
+                put(z);
+                wave_order();
+                float e = chosen ? s_row[id] : 0.0f, all = total<kLanes>(e);
+                if (all < 1e-30f) {     // choices far below the row's largest: from the largest of them
+                    const uint8_t* row = row_of(a.logits, t, a.stride, kFp32);
+                    float c = -__builtin_inff();
+                    if (chosen) c = kFp32 ? reinterpret_cast<const float*>(row)[id]
+                                          : __uint_as_float(uint32_t(reinterpret_cast<const uint16_t*>(row)[id]) << 16);
+                    const float most = across<kLanes>(c, [](float x, float y) { return larger(x, y); });
+                    e = exp_of(c - (most == -__builtin_inff() ? 0.0f : most));
+                    all = total<kLanes>(e);
+                }
                 const float w = all == 0.0f ? 0.0f : e / all;
                 d = w * (d - total<kLanes>(w * d));
+                wave_order();
+                put(none);
             }
             // a lane whose number another one has overwritten shares its expert: then one after the
             // other adds
-            const bool chosen = id >= 0;
+            wave_order();
             if (chosen) s_row[id] = __uint_as_float(lane + 1);
             wave_order();
             const bool shared = chosen && __float_as_uint(s_row[id]) != lane + 1;
@@ -586,6 +659,7 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(const GateArgs a)
             wave_order();
             if (chosen) s_row[id] = 0.0f;
         }
+        const float over = 1.0f / sum;
         if (a.renormalize) {
             if (a.totals) {
                 float dot = 0.0f;
@@ -658,7 +732,7 @@ hipError_t launch_moe_gate(const GateArgs& args, hipStream_t s)
         return hipGetLastError();
     });
     if (e != hipSuccess || !balance) return e;
-    hipLaunchKernelGGL(gate_finish_kernel, dim3((a.num_experts + kFinishColumns - 1) / kFinishColumns), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(gate_finish_kernel, dim3((a.num_experts + kFinishColumns - 1) / kFinishColumns), dim3(kFinishThreads), 0, s, a);
     return hipGetLastError();
 }
 
