@@ -10,8 +10,8 @@
 //             and dL E / (K n^2) c[e]
 //
 // Logits are read once, by a group of lanes per token that holds the row in registers.
-// Everything is fp32; sums over tokens are joined in a fixed order (lanes, waves, workgroups),
-// the last step in 64 bits, so a call gives the same bits on every run.
+// Values are fp32; sums over tokens are joined in a fixed order (lanes, waves, workgroups), the
+// workgroups' in 64 bits, so a call gives the same bits on every run.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -35,10 +35,13 @@ __device__ inline void wave_order()
     __builtin_amdgcn_wave_barrier();
 }
 
-template <int kTurn>
-__device__ inline uint32_t turned(uint32_t v)   // from kTurn lanes on, within 16
+// A lane's partner in the step of a reduction that brings together runs of `kRun` lanes that
+// agree already: lanes apart by 1, by 2, then mirrored within 8 and within 16.
+template <int kRun>
+__device__ inline uint32_t partner(uint32_t v)
 {
-    return uint32_t(__builtin_amdgcn_update_dpp(int(v), int(v), 0x120 + kTurn, 0xF, 0xF, false));
+    constexpr int kControl = kRun == 1 ? 0xB1 : kRun == 2 ? 0x4E : kRun == 4 ? 0x141 : 0x140;
+    return uint32_t(__builtin_amdgcn_update_dpp(int(v), int(v), kControl, 0xF, 0xF, false));
 }
 
 // ---- keys: unsigned 32 bits in the order of the values, NaNs above all, both zeros alike ----
@@ -69,7 +72,7 @@ struct KeyBf16 {
     static __device__ inline KeyBf16 larger(KeyBf16 a, KeyBf16 b) { a.v = max(a.v, b.v); return a; }
     static __device__ inline KeyBf16 smaller(KeyBf16 a, KeyBf16 b) { a.v = min(a.v, b.v); return a; }
     static __device__ inline KeyBf16 either(bool first, KeyBf16 a, KeyBf16 b) { a.v = first ? a.v : b.v; return a; }
-    template <int kTurn> __device__ inline KeyBf16 turn() const { KeyBf16 k; k.v = turned<kTurn>(v); return k; }
+    template <int kRun> __device__ inline KeyBf16 turn() const { KeyBf16 k; k.v = partner<kRun>(v); return k; }
     __device__ inline KeyBf16 across(int mask) const { KeyBf16 k; k.v = uint32_t(__shfl_xor(int(v), mask)); return k; }
 };
 
@@ -101,10 +104,10 @@ struct KeyFp32 {
         a.v = __hiloint2double(first ? int(a.hi()) : int(b.hi()), first ? int(a.lo()) : int(b.lo()));
         return a;
     }
-    template <int kTurn> __device__ inline KeyFp32 turn() const
+    template <int kRun> __device__ inline KeyFp32 turn() const
     {
         KeyFp32 k;
-        k.v = __hiloint2double(int(turned<kTurn>(hi())), int(turned<kTurn>(lo())));
+        k.v = __hiloint2double(int(partner<kRun>(hi())), int(partner<kRun>(lo())));
         return k;
     }
     __device__ inline KeyFp32 across(int mask) const
@@ -119,10 +122,10 @@ struct KeyFp32 {
 template <uint32_t kLanes, class Key>
 __device__ inline Key largest(Key k)
 {
-    k = Key::larger(k, k.template turn<8>());
-    k = Key::larger(k, k.template turn<4>());
-    k = Key::larger(k, k.template turn<2>());
     k = Key::larger(k, k.template turn<1>());
+    k = Key::larger(k, k.template turn<2>());
+    if constexpr (kLanes > 4) k = Key::larger(k, k.template turn<4>());
+    if constexpr (kLanes > 8) k = Key::larger(k, k.template turn<8>());
     if constexpr (kLanes == 64) {
         k = Key::larger(k, k.across(16));
         k = Key::larger(k, k.across(32));
@@ -135,10 +138,10 @@ template <uint32_t kLanes, class Op>
 __device__ inline float across(float v, Op op)
 {
     const auto with = [&](uint32_t o) { v = op(v, __uint_as_float(o)); };
-    with(turned<8>(__float_as_uint(v)));
-    with(turned<4>(__float_as_uint(v)));
-    with(turned<2>(__float_as_uint(v)));
-    with(turned<1>(__float_as_uint(v)));
+    with(partner<1>(__float_as_uint(v)));
+    with(partner<2>(__float_as_uint(v)));
+    if constexpr (kLanes > 4) with(partner<4>(__float_as_uint(v)));
+    if constexpr (kLanes > 8) with(partner<8>(__float_as_uint(v)));
     if constexpr (kLanes == 64) {
         with(uint32_t(__shfl_xor(int(__float_as_uint(v)), 16)));
         with(uint32_t(__shfl_xor(int(__float_as_uint(v)), 32)));
@@ -345,7 +348,7 @@ __device__ inline float exps(float (&z)[kPer])
 //
 // A lane sorts its keys, then the lanes' firsts are compared top_k times and the one chosen
 // taken off its lane's list.  Bound by the instructions: 16384 x 256 in fp32, 8 of them, take
-// 4096 waves of about 700.
+// 4096 waves of about 1070: 12 us, of which memory would need 4.
 template <uint32_t kLanes, uint32_t kPer, uint32_t kTop, class Key>
 __global__ __launch_bounds__(1024) void gate_kernel(const GateArgs a)
 {
@@ -369,23 +372,10 @@ __global__ __launch_bounds__(1024) void gate_kernel(const GateArgs a)
     float sums[kPer] = {};
     uint32_t tokens = 0;
     const uint64_t step = uint64_t(gridDim.x) * waves * kGroups;
-    uint64_t t = uint64_t(blockIdx.x) * waves * kGroups + threadIdx.x / kLanes;
-    // Short rows are requested one ahead (65536 x 64, given choices: 8.6 us, ).
-    constexpr bool kAhead = kPer <= 4;
-    float ahead[kPer];
-    bool there_ahead = false;
-    const auto load = [&](uint64_t at) {
-        S::load(ahead, row_of(a.logits, at, a.stride, fp32), lane, E, fp32);
-        there_ahead = !a.mask || a.mask[at] != 0;
-    };
-    if (kAhead && t < a.tokens) load(t);
-    for (; t < a.tokens; t += step) {
+    for (uint64_t t = uint64_t(blockIdx.x) * waves * kGroups + threadIdx.x / kLanes; t < a.tokens; t += step) {
         float z[kPer];
-        if (!kAhead) load(t);
-#pragma unroll
-        for (uint32_t i = 0; i < kPer; i++) z[i] = ahead[i];
-        const bool there = there_ahead;
-        if (kAhead && t + step < a.tokens) load(t + step);
+        S::load(z, row_of(a.logits, t, a.stride, fp32), lane, E, fp32);
+        const bool there = !a.mask || a.mask[t] != 0;
         if (!there) {
 #pragma unroll
             for (uint32_t i = 0; i < kPer; i++) z[i] = -__builtin_inff();
@@ -452,10 +442,8 @@ __global__ __launch_bounds__(1024) void gate_kernel(const GateArgs a)
     float* s_sums = reinterpret_cast<float*>(s_count + E);
 #pragma unroll
     for (uint32_t i = 0; i < kPer; i++) {
-        if constexpr (kLanes == 16) {
-            sums[i] += __shfl_xor(sums[i], 16);
-            sums[i] += __shfl_xor(sums[i], 32);
-        }
+#pragma unroll
+        for (uint32_t d = kLanes; d < 64; d *= 2) sums[i] += __shfl_xor(sums[i], int(d));
         const uint32_t e = S::expert(lane, i);
         if (lane_id() < kLanes && e < E) s_sums[wave * E + e] = sums[i];
     }
@@ -688,25 +676,40 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(const GateArgs a)
     }
 }
 
-// Lanes per token and values per lane.  A lane holds a token's choice `lane`, so 16 lanes do
-// up to 16 choices.
-template <class Run>
+// Lanes per token and values per lane.  Lane k holds choice k, so there are at least as many
+// lanes as choices.
+//
+// Gradient: the fewer lanes share a token, the fewer steps join them and the more tokens a wave
+// takes at once, up to 16 values for a lane (the loss's of 65536 x 64: 10.3 us with 16 lanes, 8.3
+// with 4).  Forward, a lane sorts its values, so more lanes have less to do: 16, or 64 (8191 x
+// 61, 3 of them: 4.9 us with 16 lanes, 7.8 with 4; 65536 x 64 without choices to make 9.4 and
+// 9.8).
+template <bool kGradient, class Run>
 hipError_t by_shape(const GateArgs& a, Run run)
 {
-    const auto with = [&](auto lanes, auto per) { return run(lanes, per); };
     using std::integral_constant;
-    integral_constant<uint32_t, 16> few;
+    const uint32_t e = a.num_experts, k = a.top_k;
     integral_constant<uint32_t, 64> wave;
-    if (a.num_experts > 256 || a.top_k > 16) {
-        if (a.num_experts > 512) return with(wave, integral_constant<uint32_t, 16>());
-        if (a.num_experts > 256) return with(wave, integral_constant<uint32_t, 8>());
-        return with(wave, integral_constant<uint32_t, 4>());
+    integral_constant<uint32_t, 16> sixteen;
+    integral_constant<uint32_t, 8> eight;
+    integral_constant<uint32_t, 4> four;
+    if (e > 256 || k > 16) {
+        if (e > 512) return run(wave, sixteen);
+        if (e > 256) return run(wave, eight);
+        return run(wave, four);
     }
-    if (a.num_experts > 128) return with(few, integral_constant<uint32_t, 16>());
-    if (a.num_experts > 64) return with(few, integral_constant<uint32_t, 8>());
-    if (a.num_experts > 32) return with(few, integral_constant<uint32_t, 4>());
-    if (a.num_experts > 16) return with(few, integral_constant<uint32_t, 2>());
-    return with(few, integral_constant<uint32_t, 1>());
+    if constexpr (kGradient) {
+        if (k <= 4 && e <= 32) return run(four, eight);
+        if (k <= 4 && e <= 64) return run(four, sixteen);
+        if (k <= 8 && e <= 64) return run(eight, eight);
+        if (k <= 8 && e <= 128) return run(eight, sixteen);
+    } else {
+        if (e <= 16) return run(sixteen, integral_constant<uint32_t, 1>());
+        if (e <= 32) return run(sixteen, integral_constant<uint32_t, 2>());
+    }
+    if (e <= 64) return run(sixteen, four);
+    if (e <= 128) return run(sixteen, eight);
+    return run(sixteen, sixteen);
 }
 
 }  // namespace
@@ -715,7 +718,7 @@ hipError_t launch_moe_gate(const GateArgs& args, hipStream_t s)
 {
     GateArgs a = args;
     const bool balance = a.counts != nullptr;
-    const hipError_t e = by_shape(a, [&](auto lanes, auto per) {
+    const hipError_t e = by_shape<false>(a, [&](auto lanes, auto per) {
         constexpr uint32_t kLanes = decltype(lanes)::value, kPer = decltype(per)::value;
         constexpr uint32_t kTop = kPer < 8 ? kPer : 8;
         // as many workgroups as the workspace has room for, of as many waves as that leaves
@@ -738,7 +741,7 @@ hipError_t launch_moe_gate(const GateArgs& args, hipStream_t s)
 
 hipError_t launch_moe_gate_backward(const GateArgs& a, hipStream_t s)
 {
-    return by_shape(a, [&](auto lanes, auto per) {
+    return by_shape<true>(a, [&](auto lanes, auto per) {
         constexpr uint32_t kLanes = decltype(lanes)::value, kPer = decltype(per)::value;
         constexpr uint32_t kTokens = 256 / kLanes;
         const uint64_t groups = (a.tokens + kTokens - 1) / kTokens;
