@@ -568,7 +568,8 @@ zipccl_status zipccl_moe_gate_backward(const void* logits, int dtype, uint64_t s
  *             outputs 16 a + o and inputs 128 b + 32 i + 8 g + j (o < 16; i, g < 4; j < 8) the
  *             little-endian dword 4 * (16 g + o) + i holds q as two's complement in bits 4 j ..
  *             4 j + 3.  Places past outputs or row_len hold 0.
- *   scales    num_experts x ceil(row_len / group) x outputs, BF16 or FP32 (scale_dtype) */
+ *   scales    num_experts x ceil(row_len / group) x outputs, BF16 or FP32 (scale_dtype)
+ * Both calls refuse (SIZE) outputs >= 2^24, row_len > 2^24 and an expert of 2^31 scales. */
 #define ZIPCCL_TILE4_OUTPUTS 16
 #define ZIPCCL_TILE4_INPUTS 128
 #define ZIPCCL_TILE4_BYTES 1024
@@ -596,8 +597,7 @@ zipccl_status zipccl_quantize_weights4(const void* w, uint64_t w_stride, int num
  *   offsets   as in zipccl_experts_product (rows outside every expert's range are left as they
  *             were)
  *   q, scales as above; q is 16-byte aligned
- * Errors: INVALID, ALIGN, SIZE (row_len > 2^24, outputs >= 2^24, rows * outputs beyond one
- * launch), HIP. */
+ * Errors: INVALID, ALIGN, SIZE (as above; rows * outputs beyond one launch), HIP. */
 zipccl_status zipccl_experts_product4(const void* x, uint64_t x_stride, uint64_t x_rows, const int32_t* index,
                                       uint64_t rows, const void* q, const void* scales, int scale_dtype,
                                       uint64_t group, int num_experts, uint64_t outputs, uint64_t row_len,

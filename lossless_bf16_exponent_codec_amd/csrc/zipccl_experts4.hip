@@ -102,39 +102,45 @@ __global__ __launch_bounds__(64) void quantize_weights4_kernel(const Pack4Args a
 // Product
 // ------------------------------------------------------------------------------------
 
-// Two weights, those of byte kByte of w (u: w >> 4), as BF16 divided by 16: the conversion of
-// 4-bit numbers gives q / 16 in fp32, exact in 4 significant bits, whose upper half is the BF16.
-// In assembly because the compiler shifts bytes that the instruction could select, and, between
-// single pieces of assembly, waits.
+// Weights as BF16 divided by 16: the conversion of 4-bit numbers gives q / 16 in fp32, exact in
+// 4 significant bits, whose upper half is the BF16.  The conversions are in assembly because the
+// compiler shifts bytes that the instruction could select, and waits between single pieces of
+// assembly; the halves are joined outside, where the compiler sees what a matrix instruction
+// reads and keeps the wait states between.
+struct Pair4 {
+    uint32_t lo, hi;
+    __device__ inline uint32_t joined() const { return __builtin_amdgcn_perm(hi, lo, 0x07060302u); }
+};
+
+#define ZC_CVT(d, s) "v_cvt_off_f32_i4 %" #d ", %" #s "\n\t"
+#define ZC_CVT_BYTE(b, d, s) "v_cvt_off_f32_i4_sdwa %" #d ", %" #s " dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_" #b "\n\t"
+
+// The two weights of byte kByte of w (u: w >> 4).
 template <int kByte>
-__device__ inline uint32_t weights2(uint32_t w, uint32_t u)
+__device__ inline Pair4 weights2(uint32_t w, uint32_t u)
 {
-    uint32_t d, t;
-    const uint32_t halves = 0x07060302u;
-    if constexpr (kByte == 0)
-        asm("v_cvt_off_f32_i4 %0, %2\n\tv_cvt_off_f32_i4 %1, %3\n\tv_perm_b32 %0, %1, %0, %4"
-            : "=&v"(d), "=&v"(t) : "v"(w), "v"(u), "s"(halves));
-    else if constexpr (kByte == 1)
-        asm("v_cvt_off_f32_i4_sdwa %0, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1\n\t"
-            "v_cvt_off_f32_i4_sdwa %1, %3 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1\n\tv_perm_b32 %0, %1, %0, %4"
-            : "=&v"(d), "=&v"(t) : "v"(w), "v"(u), "s"(halves));
-    else if constexpr (kByte == 2)
-        asm("v_cvt_off_f32_i4_sdwa %0, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2\n\t"
-            "v_cvt_off_f32_i4_sdwa %1, %3 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2\n\tv_perm_b32 %0, %1, %0, %4"
-            : "=&v"(d), "=&v"(t) : "v"(w), "v"(u), "s"(halves));
-    else
-        asm("v_cvt_off_f32_i4_sdwa %0, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3\n\t"
-            "v_cvt_off_f32_i4_sdwa %1, %3 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3\n\tv_perm_b32 %0, %1, %0, %4"
-            : "=&v"(d), "=&v"(t) : "v"(w), "v"(u), "s"(halves));
-    return d;
+    Pair4 p;
+    if constexpr (kByte == 0) asm(ZC_CVT(0, 2) ZC_CVT(1, 3) : "=&v"(p.lo), "=&v"(p.hi) : "v"(w), "v"(u));
+    else if constexpr (kByte == 1) asm(ZC_CVT_BYTE(1, 0, 2) ZC_CVT_BYTE(1, 1, 3) : "=&v"(p.lo), "=&v"(p.hi) : "v"(w), "v"(u));
+    else if constexpr (kByte == 2) asm(ZC_CVT_BYTE(2, 0, 2) ZC_CVT_BYTE(2, 1, 3) : "=&v"(p.lo), "=&v"(p.hi) : "v"(w), "v"(u));
+    else asm(ZC_CVT_BYTE(3, 0, 2) ZC_CVT_BYTE(3, 1, 3) : "=&v"(p.lo), "=&v"(p.hi) : "v"(w), "v"(u));
+    return p;
 }
 
 // Eight weights of a dword, in the order of a matrix instruction's operand.
 __device__ inline v8b weights8(uint32_t w)
 {
-    const uint32_t u = w >> 4;
-    return __builtin_bit_cast(v8b, v4i{int(weights2<0>(w, u)), int(weights2<1>(w, u)), int(weights2<2>(w, u)), int(weights2<3>(w, u))});
+    Pair4 p[4];
+    asm(ZC_CVT(0, 8) ZC_CVT(1, 9) ZC_CVT_BYTE(1, 2, 8) ZC_CVT_BYTE(1, 3, 9) ZC_CVT_BYTE(2, 4, 8) ZC_CVT_BYTE(2, 5, 9)
+        ZC_CVT_BYTE(3, 6, 8) ZC_CVT_BYTE(3, 7, 9)
+        : "=&v"(p[0].lo), "=&v"(p[0].hi), "=&v"(p[1].lo), "=&v"(p[1].hi), "=&v"(p[2].lo), "=&v"(p[2].hi),
+          "=&v"(p[3].lo), "=&v"(p[3].hi)
+        : "v"(w), "v"(w >> 4));
+    return __builtin_bit_cast(v8b, v4i{int(p[0].joined()), int(p[1].joined()), int(p[2].joined()), int(p[3].joined())});
 }
+
+#undef ZC_CVT
+#undef ZC_CVT_BYTE
 
 // What lanes of this wave wrote to LDS before can be read by its other lanes after.
 __device__ inline void wave_order()
@@ -423,7 +429,7 @@ constexpr uint32_t slot4(uint32_t n) { return kTileRows4 * 256 + 4 * n * kTileBy
 //
 // Bound by the instructions issued: per slab and wave (kN 2) 32 products of 16 cycles, 104
 // instructions of conversion, 32 to scale, about 60 for loads and LDS.  8192 rows of 8 experts,
-// 7168 -> 4096: 553 us, 0.87 PFLOP/s (444 without its loads, 342 without its products; the
+// 7168 -> 4096: 540 us, 0.89 PFLOP/s (444 without its loads, 342 without its products; the
 // library's product in BF16, weights unpacked: 367).  Two workgroups out of step on a CU do
 // better than one of 8 waves that share 128 rows x 256 outputs (601): those convert, and
 // multiply, all at the same time.
@@ -527,23 +533,26 @@ __global__ __launch_bounds__(256, (kN == 1 ? 4 : 3) - (kParts > 1)) void product
                     uint32_t upper[kN];
 #pragma unroll
                     for (uint32_t n = 0; n < kN; n++) upper[n] = i < 3 ? uint32_t(packed[n][(i + 1) & 3]) >> 4 : 0;
-                    // products, and between them the next weights' conversion
+                    // products, each between the conversion of some of the next weights and its joining
 #pragma unroll
                     for (uint32_t m = 0; m < kMine; m++)
 #pragma unroll
                         for (uint32_t n = 0; n < kN; n++) {
+                            constexpr uint32_t kPieces = 4 / kMine;
+                            Pair4 pair[4];
+                            const uint32_t w = uint32_t(packed[n][(i + 1) & 3]);
+                            const auto piece = [&](uint32_t b) { return i < 3 && m * kPieces <= b && b < (m + 1) * kPieces; };
+                            if (piece(0)) pair[0] = weights2<0>(w, upper[n]);
+                            if (piece(1)) pair[1] = weights2<1>(w, upper[n]);
+                            if (piece(2)) pair[2] = weights2<2>(w, upper[n]);
+                            if (piece(3)) pair[3] = weights2<3>(w, upper[n]);
+                            __builtin_amdgcn_sched_barrier(0);
                             const v4f c = i % (4 / kParts) == 0 ? v4f{} : sum[m][n];
                             sum[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i & 1][m], __builtin_bit_cast(v8b, q[i & 1][n]), c, 0, 0, 0);
-                            if (i < 3) {
-                                const uint32_t w = uint32_t(packed[n][(i + 1) & 3]);
-                                v4i& to = q[(i + 1) & 1][n];
-                                constexpr uint32_t kPieces = 4 / kMine;
-                                if (m * kPieces <= 0 && 0 < (m + 1) * kPieces) to[0] = int(weights2<0>(w, upper[n]));
-                                if (m * kPieces <= 1 && 1 < (m + 1) * kPieces) to[1] = int(weights2<1>(w, upper[n]));
-                                if (m * kPieces <= 2 && 2 < (m + 1) * kPieces) to[2] = int(weights2<2>(w, upper[n]));
-                                if (m * kPieces <= 3 && 3 < (m + 1) * kPieces) to[3] = int(weights2<3>(w, upper[n]));
-                            }
                             __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                            for (uint32_t b = 0; b < 4; b++)
+                                if (piece(b)) q[(i + 1) & 1][n][b] = int(pair[b].joined());
                         }
                     if ((i + 1) % (4 / kParts) == 0) {
 #pragma unroll

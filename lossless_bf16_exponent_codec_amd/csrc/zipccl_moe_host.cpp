@@ -120,6 +120,14 @@ bool is_group(uint64_t group) { return group == 32 || group == 64 || (group > 0 
 
 constexpr uint64_t kMaxOutputs = 1ull << 24;
 constexpr uint64_t kMaxRowLen4 = 1ull << 24;
+constexpr uint64_t kMaxScales4 = 1ull << 31;   // of an expert: their indices are 32 bits
+
+zipccl_status check_weights4(uint64_t outputs, uint64_t row_len, uint64_t group)
+{
+    if (outputs >= kMaxOutputs || row_len > kMaxRowLen4 || (row_len - 1) / group + 1 >= (kMaxScales4 + outputs - 1) / outputs)
+        return ZIPCCL_ERR_SIZE;
+    return ZIPCCL_OK;
+}
 
 }  // namespace
 
@@ -398,7 +406,7 @@ zipccl_status zipccl_quantize_weights4(const void* w, uint64_t w_stride, int num
     if (!is_dtype(scale_dtype) || !is_group(group) || num_experts < 1 || num_experts > kMaxExperts || outputs < 1 ||
         row_len < 1 || !w || !q || !scales)
         return ZIPCCL_ERR_INVALID;
-    if (outputs >= kMaxOutputs || row_len > kMaxRowLen4) return ZIPCCL_ERR_SIZE;
+    if (zipccl_status r = check_weights4(outputs, row_len, group)) return r;
     if (zipccl_status r = check_rows(w, uint64_t(num_experts) * outputs, row_len, w_stride, ZIPCCL_BF16)) return r;
     if (!aligned(q, 16) || !aligned(scales, value_bytes(scale_dtype))) return ZIPCCL_ERR_ALIGN;
     Pack4Args a{};
@@ -424,8 +432,8 @@ zipccl_status zipccl_experts_product4(const void* x, uint64_t x_stride, uint64_t
         num_experts > kMaxExperts || outputs < 1 || row_len < 1 || !q || !scales)
         return ZIPCCL_ERR_INVALID;
     if ((!offsets && num_experts != 1) || (!index && rows != x_rows)) return ZIPCCL_ERR_INVALID;
-    if (rows >= kMaxCount || x_rows >= kMaxCount || outputs >= kMaxOutputs || row_len > kMaxRowLen4)
-        return ZIPCCL_ERR_SIZE;
+    if (rows >= kMaxCount || x_rows >= kMaxCount) return ZIPCCL_ERR_SIZE;
+    if (zipccl_status r = check_weights4(outputs, row_len, group)) return r;
     if (zipccl_status r = check_rows(x, x_rows, row_len, x_stride, ZIPCCL_BF16)) return r;
     if (zipccl_status r = check_rows(out, rows, outputs, out_stride, out_dtype)) return r;
     if (!aligned(q, 16) || !aligned(scales, value_bytes(scale_dtype)) || !aligned(index, 4) || !aligned(offsets, 4) ||

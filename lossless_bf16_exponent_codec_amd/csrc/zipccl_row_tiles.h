@@ -85,7 +85,9 @@ struct RowTiles {
             const uint64_t past = __ballot(before + sum > tile);
             if (past) {
                 const uint32_t l = uint32_t(__builtin_ctzll(past));
-                const uint32_t at = tile - before - (__builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(tiles, l));
+                const uint32_t of = __builtin_amdgcn_readlane(tiles, l);
+                const uint32_t at = tile - before - (__builtin_amdgcn_readlane(sum, l) - of);
+                if (at >= of) return false;     // offsets that fall made sums pass 32 bits
                 expert = e0 + l;
                 row0 = __builtin_amdgcn_readlane(begin, l) + at * kRows;
                 rows = min(kRows, __builtin_amdgcn_readlane(end, l) - row0);

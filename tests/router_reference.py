@@ -133,9 +133,10 @@ def product4(x, index, values, scales, group, offsets):
     out, size = np.full((M, N), np.nan), np.zeros((M, N))
     for e in range(E):
         w = values[e] * np.repeat(scales[e].T, group, axis=1)[:, :H]
-        for s in range(int(offsets[e]), int(offsets[e + 1])):
-            row = x[index[s]] if 0 <= index[s] < x.shape[0] else np.zeros(H)
-            with np.errstate(invalid="ignore"):
-                out[s] = w @ row
-                size[s] = np.abs(w) @ np.abs(row)
+        at = slice(int(offsets[e]), int(offsets[e + 1]))
+        there = (index[at] >= 0) & (index[at] < x.shape[0])
+        rows = np.where(there[:, None], x[np.where(there, index[at], 0)], 0.0)
+        with np.errstate(invalid="ignore"):
+            out[at] = rows @ w.T
+            size[at] = np.abs(rows) @ np.abs(w).T
     return out, size

@@ -153,6 +153,46 @@ def test_product(Z, moe, T, M, E, N, H, group, dtype, scale_dtype):
     check(Z, x, index, q, s, values, group, offsets, dtype, whole=True)
 
 
+# enough rows for tiles of 64 (128 outputs wide, and 64), and enough outputs for workgroups of 32
+# and 64 of them on few rows
+MANY = [(300, 1200, 8, 1500, 130, 32), (700, 1100, 2, 2050, 257, 64), (90, 1200, 8, 1400, 640, 128),
+        (300, 1200, 8, 2500, 300, 128), (64, 1100, 2, 3900, 515, 256), (200, 1300, 8, 2400, 128, 64),
+        (1300, 1300, 1, 3200, 386, 32), (64, 640, 40, 160, 400, 64), (400, 1600, 4, 300, 260, 32),
+        (1000, 1000, 100, 200, 700, 128)]
+
+
+@pytest.mark.parametrize("scale_dtype,dtype", [(torch.bfloat16, torch.float32), (torch.float32, torch.bfloat16)])
+@pytest.mark.parametrize("T,M,E,N,H,group", MANY)
+def test_many_rows(Z, moe, T, M, E, N, H, group, dtype, scale_dtype):
+    rng = np.random.default_rng(M + N + H)
+    # rows that are loaded without registers, and rows at odd places
+    for stride, offset in ((-(-H // 8) * 8, 0), (H + 1, 3)):
+        x, index, q, s, values = make(rng, moe, T, M, E, N, H, group, scale_dtype, stride=stride, offset=offset)
+        check(Z, x, index, q, s, values, group, spread(rng, M, E), dtype)
+    x, index, q, s, values = make(rng, moe, T, M, E, N, H, group, scale_dtype, whole=True)
+    check(Z, x, index, q, s, values, group, spread(rng, M, E, empty=0.0), dtype, whole=True)
+
+
+@pytest.mark.parametrize("T,M,E,N,H,group", MANY[:8:3])
+def test_many_rows_some_bad(Z, moe, T, M, E, N, H, group):
+    # rows out of range, rows behind the last expert, NaN and infinity in a token
+    rng = np.random.default_rng(N)
+    x, index, q, s, values = make(rng, moe, T, M, E, N, H, group, torch.bfloat16, whole=True)
+    index[3::50], index[4::70] = T, -1
+    x[7, H - 1], x[8, 0] = float("nan"), float("inf")
+    offsets = np.concatenate([[2], np.sort(rng.integers(2, M - 40, E - 1)), [M - 40]]).astype(np.int32)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full((M, N), POISON, device="cuda")
+    Z.experts_product4(x, q, s, group, out, rows=index, offsets=torch.from_numpy(offsets).cuda(), status=status)
+    assert int(status.item()) == Z.STATUS_BAD_INDEX
+    want, _ = R.product4(host(x), index.cpu().numpy(), values, host(s), group, offsets)
+    got, at = host(out), index.cpu().numpy()
+    assert np.all(got[:2] == POISON) and np.all(got[M - 40:] == POISON)
+    inside = slice(2, M - 40)
+    assert not got[inside][(at[inside] < 0) | (at[inside] >= T)].any()
+    assert np.array_equal(got[inside], want[inside], equal_nan=True)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("H,stride,offset", [(64, 67, 1), (515, 520, 3), (128, 128, 7), (1000, 1001, 1)])
 def test_strided_and_unaligned_rows(Z, moe, H, stride, offset, dtype):

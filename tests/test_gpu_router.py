@@ -102,7 +102,7 @@ def check_gate(Z, z, logits, K, renormalize, mask=None, with_balance=True):
 
 SHAPES = [(1, 1, 1), (1, 8, 256), (5, 2, 3), (7, 3, 16), (64, 8, 64), (65, 1, 17), (33, 4, 33), (100, 16, 100),
           (41, 5, 128), (130, 8, 129), (257, 2, 256), (37, 6, 257), (50, 64, 64), (19, 17, 200), (30, 64, 512),
-          (23, 8, 513), (12, 64, 1024), (1500, 3, 61), (9000, 2, 5)]
+          (23, 8, 513), (12, 64, 1024), (1500, 3, 61), (9000, 2, 5), (40, 12, 40), (31, 10, 130), (70, 16, 256)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -305,6 +305,66 @@ def test_gradient_of_any_choices(Z, renormalize):
     Z.moe_gate_backward(logits, torch.from_numpy(np.where(bad == E, -1, bad)).cuda(), e, dweights=dw,
                         renormalize=renormalize)
     assert torch.equal(d, e)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,K,E", [(60, 3, 20), (50, 8, 100), (30, 20, 300)])
+def test_gradient_of_choices_far_below_the_largest(Z, T, K, E, dtype):
+    # exp of what lies 90 to 200 below is nothing beside the row's largest; the weights over such
+    # choices are ordinary ones
+    rng = np.random.default_rng(E)
+    logits, z = make_logits(rng, T, E, dtype)
+    logits[:, 0] = torch.from_numpy(rng.uniform(90, 200, T)).to(dtype)
+    z = host(logits)
+    ids = np.stack([rng.permutation(E - 1)[:K] + 1 for _ in range(T)])
+    ids[::5, 0] = 0
+    check_backward(Z, z, logits, torch.from_numpy(ids).cuda(), True, rng)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_experts_closed_by_the_lowest_value(Z, dtype):
+    # beside open experts the type's lowest value closes one as minus infinity does; a row that
+    # holds nothing else is open everywhere
+    rng = np.random.default_rng(31)
+    T, K, E = 80, 3, 24
+    logits, z = make_logits(rng, T, E, dtype, closed=0.5)
+    z[:, :K] = np.where(np.isinf(z[:, :K]), 0.0, z[:, :K])
+    logits.copy_(torch.from_numpy(z))
+    low = torch.where(logits.isinf(), torch.finfo(dtype).min, logits)
+    a, b = outputs(T, K, E), outputs(T, K, E)
+    dw, dl = torch.randn(T, K, device="cuda"), torch.ones(1, device="cuda")
+    grads = []
+    for renormalize in (True, False):
+        for o, x in ((a, logits), (b, low)):
+            Z.moe_gate(x, o[0], o[1], renormalize=renormalize, counts=o[2], sums=o[3], loss=o[4], workspace=space(Z))
+            grads.append(torch.empty_like(x))
+            Z.moe_gate_backward(x, o[0], grads[-1], dweights=dw, counts=o[2], dloss=dl, renormalize=renormalize)
+        assert all(torch.equal(x, y) for x, y in zip(a, b)) and torch.equal(*grads[-2:])
+    low.fill_(torch.finfo(dtype).min)
+    Z.moe_gate(low, b[0], b[1], counts=b[2], sums=b[3], loss=b[4], workspace=space(Z))
+    assert b[0].tolist() == [[0, 1, 2]] * T and bool(((b[1] - 1 / 3).abs() <= 4 * U).all())
+    assert b[2].tolist() == [T] * K + [0] * (E - K) + [T]
+
+
+def test_two_calls_at_once(Z):
+    # on two streams, each with a workspace of its own, against the same calls one after the other
+    g = torch.Generator(device="cuda").manual_seed(11)
+    T, K, E = 6000, 4, 130
+    logits = [torch.randn(T, E, generator=g, device="cuda") for _ in range(2)]
+    made, spaces, streams = [], [space(Z), space(Z)], [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for rep in range(10):
+        o = [outputs(T, K, E) for _ in range(2)]
+        torch.cuda.synchronize()
+        for i in range(2):
+            Z.moe_gate(logits[i], o[i][0], o[i][1], counts=o[i][2], sums=o[i][3], loss=o[i][4], workspace=spaces[i],
+                       stream=streams[i] if rep else None)
+            if not rep:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        made.append(o)
+    for o in made[1:]:
+        assert all(torch.equal(x, y) for i in range(2) for x, y in zip(o[i], made[0][i]))
 
 
 @pytest.mark.parametrize("renormalize", [True, False])

@@ -78,7 +78,8 @@ def test_quantize4_refusals(Z):
         ("INVALID", dict(E=1025)), ("INVALID", dict(N=0)), ("INVALID", dict(H=0)), ("INVALID", dict(group=0)),
         ("INVALID", dict(group=16)), ("INVALID", dict(group=96)), ("INVALID", dict(group=192)),
         ("INVALID", dict(dtype=2)), ("INVALID", dict(w_stride=99)), ("SIZE", dict(N=1 << 24)),
-        ("SIZE", dict(H=(1 << 24) + 1, w_stride=1 << 25)), ("SIZE", dict(w_stride=1 << 40)), ("ALIGN", dict(w=P + 1)),
+        ("SIZE", dict(H=(1 << 24) + 1, w_stride=1 << 25)), ("SIZE", dict(w_stride=1 << 40)),
+        ("SIZE", dict(N=1 << 16, H=1 << 20, w_stride=1 << 20)), ("ALIGN", dict(w=P + 1)),
         ("ALIGN", dict(q=P + 8)), ("ALIGN", dict(scales=P + 1)), ("ALIGN", dict(scales=P + 2, dtype=1))])
 
 
@@ -93,6 +94,7 @@ def test_product4_refusals(Z):
         ("INVALID", dict(out_stride=49)), ("SIZE", dict(rows=1 << 31)), ("SIZE", dict(x_rows=1 << 31)),
         ("SIZE", dict(N=1 << 24, out_stride=1 << 24)), ("SIZE", dict(H=(1 << 24) + 1, x_stride=1 << 25)),
         ("SIZE", dict(rows=(1 << 31) - 1, N=1 << 20, out_stride=1 << 20)), ("SIZE", dict(x_stride=1 << 40)),
+        ("SIZE", dict(N=1 << 18, out_stride=1 << 18, H=1 << 20, x_stride=1 << 20, group=128)),
         ("ALIGN", dict(x=P + 1)), ("ALIGN", dict(index=P + 2)), ("ALIGN", dict(q=P + 8)), ("ALIGN", dict(scales=P + 1)),
         ("ALIGN", dict(scales=P + 2, s_dtype=1)), ("ALIGN", dict(offsets=P + 2)), ("ALIGN", dict(out=P + 1)),
         ("ALIGN", dict(out=P + 2, dtype=1)), ("ALIGN", dict(status=P + 2))])
