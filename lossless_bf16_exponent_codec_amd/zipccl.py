@@ -872,6 +872,8 @@ def quantize_weights4(w, group: int, q, scales, stream=None):
     if len(shape) not in (2, 3):
         raise ValueError("w is experts x outputs x inputs")
     E, N, H = shape if len(shape) == 3 else (1, *shape)
+    if E < 1:
+        raise ValueError("w has one expert at least")
     if len(shape) == 3 and E > 1 and N > 1 and w.stride(0) != N * w.stride(1):
         raise ValueError("w's experts follow one another")
     wp, _, _, ws, _ = _matrix(w[0] if len(shape) == 3 else w, "w", _BF16_ONLY)
@@ -881,7 +883,7 @@ def quantize_weights4(w, group: int, q, scales, stream=None):
         raise ValueError("group is 32, 64 or a multiple of 128")
     sp, kind = _scales4(scales, E, -(-H // group), N)
     _enqueue_plain(_lib.zipccl_quantize_weights4, (w, q, scales), stream,
-              (wp, ws, E, N, H, group, _vector(q, weights4_size(E, N, H), torch.uint8, "q"), sp, kind))
+                   (wp, ws, E, N, H, group, _vector(q, weights4_size(E, N, H), torch.uint8, "q"), sp, kind))
 
 
 def _enqueue_plain(call, tensors, stream, args):

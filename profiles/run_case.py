@@ -1,4 +1,4 @@
-"""Runs one case of perf/operators.py through the package's calls, for a profiler:
+"""Runs one case of perf/operators.py or perf/more_operators.py through the package's calls, for a profiler:
 
     python3 profiles/run_case.py CASE PASSES
 """
@@ -12,12 +12,21 @@ sys.path.insert(0, ROOT)
 import torch  # noqa: E402
 
 
+def case_of(name):
+    """The module that lists the case, and the case."""
+    for file in "operators", "more_operators":
+        spec = importlib.util.spec_from_file_location(file, os.path.join(ROOT, "perf", file + ".py"))
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        for case in module.listed():
+            if case["name"] == name:
+                return module, case
+    raise SystemExit(f"no case {name}")
+
+
 def main():
-    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
-    operators = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(operators)
+    operators, case = case_of(sys.argv[1])
     operators.own = True
-    case, = (c for c in operators.listed() if c["name"] == sys.argv[1])
     state = operators.prepare(case, 1)
     for _ in range(int(sys.argv[2])):
         operators.run(state)

@@ -134,6 +134,7 @@ def test_binding_refuses_shapes_and_types(Z):
             lambda: Z.moe_gate_backward(z, i32, z, counts=counts[:8], dloss=loss),
             lambda: Z.moe_gate_backward(z, i32, z, counts=counts, dloss=loss[:0]),
             lambda: Z.quantize_weights4(bf.float(), 64, q, s), lambda: Z.quantize_weights4(bf, 64, q[:1023], s),
+            lambda: Z.quantize_weights4(torch.zeros(0, 6, 100, dtype=torch.bfloat16), 64, q, s),
             lambda: Z.quantize_weights4(bf, 128, q, s), lambda: Z.quantize_weights4(bf, 0, q, s),
             lambda: Z.experts_product4(bf.float(), q, s, 128, out, rows=off, offsets=off),
             lambda: Z.experts_product4(bf, q[:1024], s, 128, out, offsets=off),
