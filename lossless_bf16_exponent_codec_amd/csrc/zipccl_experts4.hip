@@ -429,12 +429,13 @@ constexpr uint32_t slot4(uint32_t n) { return kTileRows4 * 256 + 4 * n * kTileBy
 //
 // Bound by the instructions issued: per slab and wave (kN 2) 32 products of 16 cycles, 104
 // instructions of conversion, 32 to scale, about 60 for loads and LDS.  8192 rows of 8 experts,
-// 7168 -> 4096: 540 us, 0.89 PFLOP/s (444 without its loads, 342 without its products; the
-// library's product in BF16, weights unpacked: 367).  Two workgroups out of step on a CU do
-// better than one of 8 waves that share 128 rows x 256 outputs (601): those convert, and
-// multiply, all at the same time.
+// 7168 -> 4096: 527 us, 0.91 PFLOP/s (444 without its loads, 342 without its products; the
+// library's product in BF16, weights unpacked: 367).  Workgroups out of step on a CU do better
+// than one of 8 waves that share 128 rows x 256 outputs (601): those convert, and multiply, all
+// at the same time.  128 rows for 4 waves convert half as much and leave two waves on a SIMD:
+// 515 here, where they fill whole rounds; with half the rows 306 (287).
 template <uint32_t kN, uint32_t kParts, class Scale>
-__global__ __launch_bounds__(256, (kN == 1 ? 4 : 3) - (kParts > 1)) void product4_tile_kernel(const Product4Args a)
+__global__ __launch_bounds__(256, kN == 1 ? 4 - (kParts > 2) : 3 - (kParts > 1)) void product4_tile_kernel(const Product4Args a)
 {
     constexpr uint32_t shift = sizeof(Scale) == 4 ? 0 : 16, kSlot = slot4(kN);
     __shared__ __attribute__((aligned(1024))) uint8_t s_ring[2 * kSlot];
@@ -514,21 +515,21 @@ __global__ __launch_bounds__(256, (kN == 1 ? 4 : 3) - (kParts > 1)) void product
                 // read through vector types: of a struct's load the compiler does not know that it
                 // is of another slot than the loads under way write, and waits for those
                 v4i packed[kN];
-                v8b x[2][kMine];
+                v8b x[kMine];
                 v4i q[2][kN];
                 v4f sum[kMine][kN];
 #pragma unroll
                 for (uint32_t n = 0; n < kN; n++) packed[n] = *reinterpret_cast<const v4i*>(at_w + 1024 * n);
-                const auto take_rows = [&](uint32_t i) {
-#pragma unroll
-                    for (uint32_t m = 0; m < kMine; m++) x[i & 1][m] = *reinterpret_cast<const v8b*>(at + m * 4096 + ((4 * i + g) ^ o) * 16);
+                const auto take_rows = [&](uint32_t i, uint32_t m) {
+                    x[m] = *reinterpret_cast<const v8b*>(at + m * 4096 + ((4 * i + g) ^ o) * 16);
                 };
-                take_rows(0);
+#pragma unroll
+                for (uint32_t m = 0; m < kMine; m++) take_rows(0, m);
 #pragma unroll
                 for (uint32_t n = 0; n < kN; n++) q[0][n] = __builtin_bit_cast(v4i, weights8(uint32_t(packed[n][0])));
 #pragma unroll
                 for (uint32_t i = 0; i < 4; i++) {
-                    if (i < 3) take_rows(i + 1);
+                    if (i == 0) __builtin_amdgcn_s_setprio(1);      // before a wave that is not at its products yet
                     __builtin_amdgcn_sched_barrier(0);
                     uint32_t upper[kN];
 #pragma unroll
@@ -548,11 +549,12 @@ __global__ __launch_bounds__(256, (kN == 1 ? 4 : 3) - (kParts > 1)) void product
                             if (piece(3)) pair[3] = weights2<3>(w, upper[n]);
                             __builtin_amdgcn_sched_barrier(0);
                             const v4f c = i % (4 / kParts) == 0 ? v4f{} : sum[m][n];
-                            sum[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i & 1][m], __builtin_bit_cast(v8b, q[i & 1][n]), c, 0, 0, 0);
+                            sum[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[m], __builtin_bit_cast(v8b, q[i & 1][n]), c, 0, 0, 0);
                             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                             for (uint32_t b = 0; b < 4; b++)
                                 if (piece(b)) q[(i + 1) & 1][n][b] = int(pair[b].joined());
+                            if (i < 3 && n == kN - 1) take_rows(i + 1, m);      // the row's last product of these inputs
                         }
                     if ((i + 1) % (4 / kParts) == 0) {
 #pragma unroll
@@ -565,6 +567,7 @@ __global__ __launch_bounds__(256, (kN == 1 ? 4 : 3) - (kParts > 1)) void product
                         }
                     }
                 }
+                __builtin_amdgcn_s_setprio(0);
                 meet_loaded();
             }
         }
