@@ -612,10 +612,12 @@ hipError_t launch_tiles4(const Product4Args& a, hipStream_t s)
 // does not know the offsets).  Times in us, outputs x row_len:
 //  - from 16 rows for an expert on, tiles of 64 rows, which convert weights once for 64 rows
 //    instead of 16, where there is a round of them (32 experts, 2048 x 7168, rows each: 8:
-//    53 streamed and 60, 16: 69 and 64, 32: 100 and 79, 64: 164 and 109); 128 outputs wide
-//    where there are nearly two workgroups for a CU (the last: 109, 148 at 64 wide), else 64
-//    (1 expert, 512 rows, 4096 x 4096: 33.0 and 32.6; 8 experts, 250 rows, 1024 x 1024: 19.1
-//    and 16.9; 128 tiles, 256 rows of 1 expert, 4096 x 7168: 50 and 52, streamed 39);
+//    53 streamed and 60, 16: 68 and 62, 32: 100 and 74, 64: 162 and 105), or, of rows that
+//    fill them, seven tenths of one (1 expert, 4096 x 7168, rows: 320: 45.3 and 48.4, 384:
+//    53.5 and 46.5; 5 experts, 240 rows, 1111 x 1000: 16.3 and 14.2; 16 experts, 1400 x 4096,
+//    50 rows: 31.2 and 35.7); 128 outputs wide where there are nearly two workgroups for a CU
+//    (64 rows of 32 experts: 105, 145 at 64 wide), else 64 (1 expert, 512 rows, 4096 x 4096:
+//    32.6 and 30.1; 8 experts, 250 rows, 1024 x 1024: 18.3 and 16.1);
 //  - else streamed, with fewer outputs and more waves for a workgroup as there are fewer tiles
 //    of 16 x 16 (1 token, 1 expert, 2048 x 7168, 128 tiles: 14.7 at 64 outputs and 4 waves,
 //    10.0 at 32 and 8, 8.6 at 16 and 8; 8 experts, 1024 x 2048, 512 tiles: 7.2, 6.4, 7.5;
@@ -629,8 +631,10 @@ Shape4 choose4(const Product4Args& a)
         return parts * ((each + rows - 1) / rows) * ((a.outputs + outs - 1) / outs);
     };
     constexpr uint32_t kCus = 256;
+    const uint64_t large = tiles(kTileRows4, 128);
     // (of rows shorter than a slab the tiles' kernel would read past the end)
-    if (a.row_len >= kSlab4 && each >= 16 && tiles(kTileRows4, 128) >= kCus) return tiles(kTileRows4, 128) < kCus * 7 / 4 ? Shape4::square : Shape4::wide;
+    if (a.row_len >= kSlab4 && each >= 16 && large >= (each >= kTileRows4 ? kCus * 11 / 16 : kCus))
+        return large < kCus * 7 / 4 ? Shape4::square : Shape4::wide;
     const uint64_t n = tiles(16, 16);
     return n <= kCus ? Shape4::narrow : n < 4 * kCus ? Shape4::middle : Shape4::stream;
 }
