@@ -799,6 +799,9 @@ def _balance(counts, sums, loss, workspace, num_experts):
             _vector(loss, 1, torch.float32, "loss"), workspace.data_ptr(), workspace.nbytes)
 
 
+_NO_BALANCE = (None, None, None, None, 0)
+
+
 def _there(*tensors):
     return tuple(t for t in tensors if t is not None)
 
@@ -813,12 +816,19 @@ def moe_gate(logits, experts, weights, renormalize: bool = True, mask=None, coun
     ep, et, K, es, _ = _matrix(experts, "experts", _INT32)
     if et != T or (es != K and T > 1):
         raise ValueError(f"experts is a contiguous int32 tensor, tokens x top_k, of {T} tokens")
-    given = _there(counts, sums, loss, workspace)
-    if len(given) not in (0, 4):
+    tensors = (logits, experts, weights)
+    if counts is not None and sums is not None and loss is not None and workspace is not None:
+        balance = _balance(counts, sums, loss, workspace, E)
+        tensors += (counts, sums, loss, workspace)
+    elif counts is None and sums is None and loss is None and workspace is None:
+        balance = _NO_BALANCE
+    else:
         raise ValueError("counts, sums, loss and workspace are given together")
-    balance = _balance(*given, E) if given else (None, None, None, None, 0)
-    _enqueue(_lib.zipccl_moe_gate, (logits, experts, weights, *given, *_there(mask)), status, stream,
-             (zp, kind, zs, T, E, _mask(mask, T), K, bool(renormalize), ep,
+    if mask is not None:
+        tensors += (mask,)
+        mask = _mask(mask, T)
+    _enqueue(_lib.zipccl_moe_gate, tensors, status, stream,
+             (zp, kind, zs, T, E, mask, K, bool(renormalize), ep,
               _vector(weights, T * K, torch.float32, "weights"), *balance))
 
 
@@ -911,7 +921,7 @@ def experts_product4(x, q, scales, group: int, out, rows=None, offsets=None, sta
         raise ValueError("group is 32, 64 or a multiple of 128, rows have a value at least")
     E = 1 if offsets is None else offsets.numel() - 1
     sp, s_kind = _scales4(scales, E, -(-H // group), N)
-    size = weights4_size(E, N, H)
+    size = E * -(-N // TILE4_OUTPUTS) * -(-H // TILE4_INPUTS) * TILE4_BYTES
     if q.dtype is not torch.uint8 or not q.is_contiguous() or q.numel() != size:
         raise ValueError(f"q is a contiguous uint8 tensor of {size} bytes")
     if rows is None and M != T:
