@@ -370,7 +370,11 @@ __global__ __launch_bounds__(kThreads, kPerSimd) void product4_stream_kernel(con
         if (s < whole) multiply(b[0]);
     }
     if (first <= whole && whole < end) {      // the last slab, which rows end in; they may have only some of its parts
-        load_weights(b[0], whole, kParts > 1 ? min(part, a.groups - 1 - whole * kParts) : 0);
+        const uint32_t last = kParts > 1 ? a.groups - 1 - whole * kParts : 0;
+        load_weights(b[0], whole, min(part, last));
+        // the others' sums are 0, and so are their scales: the last group's may be infinite
+#pragma unroll
+        for (uint32_t j = 0; j < kN; j++) b[0].scale[j] = part > last ? 0 : b[0].scale[j];
 #pragma unroll
         for (uint32_t i = 0; i < 4; i++) b[0].x[i] = values8<true>(row[i], whole * kSlab4 + 8 * o, a.row_len);
         multiply(b[0]);
@@ -489,6 +493,10 @@ __global__ __launch_bounds__(256, kN == 1 ? 4 - (kParts > 2) : 3 - (kParts > 1))
 #pragma unroll
         for (uint32_t n = 0; n < kN; n++) to[n] = (scales + group * a.outputs)[p * a.outputs + min(16 * (tile0 + n) + o, a.outputs - 1)];
     };
+    // parts that the last slab lacks have sums of 0; their scales, loaded as the last group's, which
+    // may be infinite, become 0 (compared with `step` in the loop instead: 1501 rows each to 2 of
+    // 5 experts, 1000 -> 1111, 0.7 us more)
+    const bool lacking = kParts > 1 && part > a.groups - 1 - (a.slabs - 1) * kParts;
     v4f acc[4][kN] = {};
     // kMine: tiles of 16 rows that are multiplied
     const auto run = [&](auto of_rows) {
@@ -504,7 +512,8 @@ __global__ __launch_bounds__(256, kN == 1 ? 4 - (kParts > 2) : 3 - (kParts > 1))
                 if (step >= a.slabs) break;
                 uint32_t bits[kN][kParts];
 #pragma unroll
-                for (uint32_t n = 0; n < kN; n++) spread_parts<kParts>(scale[u][n], bits[n]);
+                for (uint32_t n = 0; n < kN; n++)
+                    spread_parts<kParts>(kParts > 1 && (lacking & (step + 1 == a.slabs)) ? 0 : scale[u][n], bits[n]);
                 load_fence();
                 load(step + 1, (u ^ 1) * kSlot);
                 load_fence();
