@@ -250,11 +250,17 @@ class QuantizedExperts:
         return out
 
 
+_SIGNED = {torch.uint8: torch.int8, torch.uint16: torch.int16, torch.uint32: torch.int32, torch.uint64: torch.int64}
+
+
 def pack4(values: torch.Tensor) -> torch.Tensor:
     """Whole numbers from -8 to 7 (experts x outputs x inputs, any integer type) as 4-bit tiles of
     16 outputs x 128 inputs: one row of bytes per expert."""
     E, N, H = values.shape
-    if bool(((values < -8) | (values > 7)).any()):
+    low, signed = -8, _SIGNED.get(values.dtype)
+    if signed is not None:      # the upper half of the type's range is below 0 then
+        low, values = 0, values.view(signed)
+    if bool(((values < low) | (values > 7)).any()):
         raise ValueError("4-bit values are from -8 to 7")
     tiles, slabs = -(-N // Z.TILE4_OUTPUTS), -(-H // Z.TILE4_INPUTS)
     v = torch.zeros(E, tiles * Z.TILE4_OUTPUTS, slabs * Z.TILE4_INPUTS, dtype=torch.uint8, device=values.device)
