@@ -589,9 +589,9 @@ zipccl_status zipccl_quantize_weights4(const void* w, uint64_t w_stride, int num
 /* The experts' product with 4-bit weights: for the rows s of expert e (offsets[e] <= s <
  * offsets[e + 1]) and n < outputs
  *   out[s][n] = sum over h of x[index[s]][h] * q[e][n][h] * scale[e][h / group][n]
- * with fp32 sums in a fixed order, rounded once to out_dtype (a NaN in BF16 is 0x7FC0).  A group
- * is summed before its scale multiplies it, so an infinite scale gives an infinity of the sum's
- * sign, or NaN where the sum is 0.
+ * with fp32 sums in a fixed order, rounded once to out_dtype (a NaN in BF16 is 0x7FC0).  A group's
+ * inputs in one tile of weights are summed before the scale multiplies them: an infinite scale
+ * gives infinities of these sums' signs, and NaN for a sum of 0.
  *   x         device, x_rows rows of row_len BF16 values
  *   index     device int32[rows], as zipccl_moe_sort's rows: the row of x (a token) of each
  *             row; one outside 0..x_rows-1 in an expert's range sets ZIPCCL_STATUS_BAD_INDEX and
