@@ -535,17 +535,23 @@ __global__ __launch_bounds__(kFinishThreads) void gate_finish_kernel(const GateA
     all = join(all);
     if (blockIdx.x == 0 && tid == 0) a.counts[E] = int32_t(s_tokens);
     if (gridDim.x > 1) {
+        // Parts are exchanged, not stored and loaded: an exchange always finds the place's last
+        // value, and its returned value says that it has been done, for the atomics of every
+        // workgroup of the GPU.  The ticket's step is made from what a part's exchange returned,
+        // so the ticket cannot be taken before the part is there, and the last workgroup asks for the
+        // parts once it has its ticket.  (This order is gfx950's, not the language's: release and
+        // acquire would also write back and drop the L2, 2 us.)
         uint32_t before = 0;
         if (tid == 0) {
-            // both are done where all XCDs see them, the second once the first is; ordering by release
-            // and acquire would write back and drop the L2, 2 us
-            __hip_atomic_store(finish_parts(a) + blockIdx.x, all, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            before = __hip_atomic_fetch_add(finish_ticket(a), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            const double was = __hip_atomic_exchange(finish_parts(a) + blockIdx.x, all, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            uint32_t step = 1;
+            asm volatile("" : "+s"(step) : "v"(was) : "memory");
+            before = __hip_atomic_fetch_add(finish_ticket(a), step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
         if (__builtin_amdgcn_readfirstlane(before) + 1 != gridDim.x) return;
+        asm volatile("" ::: "memory");
         static_assert(kMaxExperts / kFinishColumns <= 64, "a lane for each workgroup");
-        all = tid < gridDim.x ? __hip_atomic_load(finish_parts(a) + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
+        all = tid < gridDim.x ? __hip_atomic_exchange(finish_parts(a) + tid, 0.0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
         all = join(all);
     }
     if (tid == 0) a.loss[0] = loss_of(a, s_tokens, all);
