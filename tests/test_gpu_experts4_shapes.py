@@ -1,14 +1,28 @@
-"""The product with 4-bit weights in every kernel that its rule picks: rows that end where the last
-slab's groups do not.  Whole numbers with scales that are powers of two give exact sums and are
-compared for equality."""
+"""The product with 4-bit weights in every kernel that its rule picks: rows long enough for each
+wave's steady loop, and rows that end where the last slab's groups do not.
+
+Tolerances as in test_gpu_experts4: an fp32 sum over H inputs is off by at most H * 2^-23 of the sum
+of its terms' magnitudes, the result by half a step of its type; whole numbers with scales that are
+powers of two give exact sums and are compared for equality."""
 import numpy as np
 import pytest
 import torch
 
 from tests import product4_shapes as S
-from tests.test_gpu_experts4 import POISON, Z, host, make, moe, spread  # noqa: F401  (Z, moe: fixtures)
+from tests.test_gpu_experts4 import POISON, Z, check, host, make, moe, spread  # noqa: F401  (Z, moe: fixtures)
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("scale_dtype,dtype", [(torch.bfloat16, torch.float32), (torch.float32, torch.bfloat16)])
+@pytest.mark.parametrize("T,M,E,N,H,group", S.STREAMED)
+def test_long_streamed_rows(Z, moe, T, M, E, N, H, group, dtype, scale_dtype):
+    rng = np.random.default_rng(M + N + H)
+    x, index, q, s, values = make(rng, moe, T, M, E, N, H, group, scale_dtype)
+    check(Z, x, index, q, s, values, group, spread(rng, M, E), dtype)
+    # exact: a term is at most 4 * 8 * 4 and a multiple of 1 / 4, so sums of 3300 are below 2^21 quarters
+    x, index, q, s, values = make(rng, moe, T, M, E, N, H, group, scale_dtype, whole=True)
+    check(Z, x, index, q, s, values, group, spread(rng, M, E), dtype, whole=True)
 
 
 @pytest.mark.parametrize("scale_dtype,dtype", [(torch.bfloat16, torch.float32), (torch.float32, torch.bfloat16)])
