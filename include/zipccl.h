@@ -527,6 +527,7 @@ zipccl_status zipccl_experts_product(const void* q, uint64_t q_stride, const flo
  *   workspace device scratch, 256-byte aligned, ZIPCCL_MOE_GATE_WORKSPACE_BYTES, or NULL
  *             where counts is; carries nothing between calls; concurrent calls need separate
  *             ones
+ *   status    as in the other calls, and never written: the choices made here are in range
  * One launch, two with the balance outputs.
  * Errors: INVALID (NULL pointers, dtype, num_experts outside 1..ZIPCCL_MAX_EXPERTS, top_k
  * outside 1..ZIPCCL_MAX_TOP_K or above num_experts, stride < num_experts), ALIGN, SIZE, HIP. */

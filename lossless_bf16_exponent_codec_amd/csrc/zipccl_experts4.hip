@@ -262,7 +262,7 @@ hipError_t by_scales(const Product4Args& a, Run run)
 // 64 tokens below).
 //
 // Bound by memory with the conversion close behind: a slab of a wave is 4 KB of weights and 330
-// instructions.  64 tokens x 4 of 32 skewed experts, 7168 -> 2048: 55 us, 4.3 TB/s of weights;
+// instructions.  64 tokens x 4 of 32 skewed experts, 7168 -> 2048: 55 to 56 us, 4.3 TB/s of weights;
 // reading them alone takes 41.  Few calls fill the GPU so; smaller ones take fewer outputs per
 // workgroup and more waves along the row.
 template <uint32_t kN>
@@ -431,10 +431,12 @@ constexpr uint32_t slot4(uint32_t n) { return kTileRows4 * 256 + 4 * n * kTileBy
 // LDS a slab ahead, the rows shared by the waves, the weights each wave's own.  Within a slab
 // the conversion of the next 32 inputs' weights stands between the products of this one's.
 //
-// Bound by the instructions issued: per slab and wave (kN 2) 32 products of 16 cycles, 104
-// instructions of conversion, 32 to scale, about 60 for loads and LDS.  8192 rows of 8 experts,
-// 7168 -> 4096: 527 us, 0.91 PFLOP/s (444 without its loads, 342 without its products; the
-// library's product in BF16, weights unpacked: 367).  Workgroups out of step on a CU do better
+// Per slab and wave (kN 2) 32 products of 16 cycles, 104 instructions of conversion, 32 to scale,
+// about 60 for loads and LDS.  8192 rows of 8 experts, 7168 -> 4096: 520 to 545 us, 0.9 PFLOP/s
+// (444 without its loads, 342 without its products; the library's product in BF16, weights
+// unpacked: 367).  Vector and matrix instructions issue in 57 % of the SIMDs' cycles, the matrix
+// units work in 36 %; the rest is waits, for a slab's loads at every slab, which three waves on a
+// SIMD do not cover.  Workgroups out of step on a CU do better
 // than one of 8 waves that share 128 rows x 256 outputs (601): those convert, and multiply, all
 // at the same time.  128 rows for 4 waves convert half as much and leave two waves on a SIMD:
 // 515 here, where they fill whole rounds; with half the rows 306 (287).

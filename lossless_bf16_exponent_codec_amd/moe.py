@@ -1,7 +1,7 @@
 """A mixture-of-experts layer's router and row traffic around the codec, from torch: choices,
 weights and a balance loss from the router's logits, the choices sorted by expert, tokens
-dispatched to their experts' rows and combined back with weights (all differentiable), and
-experts' weights in 8 or 4 bits.
+dispatched to their experts' rows and combined back with weights (all differentiable), and, for
+serving, experts' weights in 8 or 4 bits (no gradient goes through their products).
 
 Each step is one call of the same name in `zipccl`; this module adds the buffers and the
 gradients (of first order).  A status word (int32, on the device) given to a step takes the
